@@ -20,6 +20,11 @@
  * "FlashAttention 설명", §3-§6).  The backward pass recomputes the scores from
  * the saved LSE ("FlashAttention-2 …", §3 Recomputation).
  *
+ * A paged KV cache serves token by token: attn_tree_fwd attends from drafted
+ * tokens to it, attn_cache_append fills it, attn_cache_weights totals the
+ * attention its slots receive, attn_evict_plan and attn_cache_compact keep it
+ * within a budget.
+ *
  * Layouts.  Q, O, dQ, dO: bf16 [B][Hq][Sq][D]; K, V, dK, dV: bf16
  * [B][Hkv][Skv][D]; LSE: fp32 [B][Hq][Sq] (natural log), contiguous, D
  * innermost.  Supported: D in {64, 128}; 1 <= Sq, Skv <= 262144; Hq a
@@ -61,7 +66,9 @@ typedef enum attn_status {
   ATTN_ERR_WORKSPACE = -4,    /* workspace or block-mask buffer too small */
   ATTN_ERR_LAUNCH = -5,       /* a CUDA call or kernel launch failed */
   ATTN_ERR_TIMEOUT = -6,      /* a kernel gave up waiting on an internal barrier */
-  ATTN_ERR_DEVICE = -7        /* no usable sm_100 device, or the kernel image failed to load */
+  ATTN_ERR_DEVICE = -7,       /* no usable sm_100 device, or the kernel image failed to load */
+  ATTN_ERR_INDEX = -8         /* a value in a device array (a cache page, length, count, parent, path or
+                                 move) is out of its bounds; recorded by a kernel in the status word */
 } attn_status;
 
 /*
@@ -345,6 +352,141 @@ ATTN25_API int attn_fwd_fp8(const uint8_t* q8, const uint8_t* k8, const float* q
                             int B, int Hq, int Hkv, int Sq, int Skv, int D, float scale,
                             int mod_kind, const attn_mod_params* mod_params,
                             const attn_block_mask* block_mask, attn_stream_t stream);
+
+/*
+ * KV cache for serving.  Keys and values live in pages of page_size rows; a
+ * batch row's slot j (0-based) is row j % page_size of its page
+ * page_table[b][j / page_size].  The pools are [num_pages][Hkv][page_size][D]
+ * bf16 views whose D elements are contiguous, with element strides (page,
+ * head, row) that are positive multiples of 8, so both the
+ * [page][head][row][D] and the [page][row][head][D] storage fit, and one
+ * page per batch row (page_size = capacity) is a plain contiguous cache.
+ *
+ * D in {64, 128}.  page_size: 16, 32, 64, 128 or a multiple of 128.  A
+ * row's capacity max_pages * page_size is at most 1048576 slots.  lens[b] is
+ * the number of filled slots; table entries behind the last page in use are
+ * not read, and rows behind lens[b] may hold anything (NaN included).
+ * page_table NULL: row b's pages are b * max_pages, b * max_pages + 1, ...
+ *
+ * lens, page_table and the other index arrays below are device memory and
+ * are read when the kernels run, so captured graphs see their later values.
+ * What the host cannot check the kernels do: a length or count outside its
+ * range is clamped; a page outside [0, num_pages) reads as rows of zeros and
+ * is never written; each such value is recorded as ATTN_ERR_INDEX in the
+ * status word (attn_get_status).  Pages may be shared between batch rows as
+ * long as no shared page is written.
+ *
+ * Calls on one cache are ordered by their streams like any other use of the
+ * same memory; the library keeps no state of a cache.
+ */
+typedef struct attn_cache {
+  attn_bf16* k;                 /* device pools, 16-byte aligned */
+  attn_bf16* v;
+  attn_strides k_strides;       /* elements between pages (b), heads (h) and rows (s) */
+  attn_strides v_strides;
+  const int32_t* page_table;    /* device int32 [B][max_pages] (4-byte aligned) or NULL */
+  int32_t* lens;                /* device int32 [B] */
+  int32_t B, Hkv, D, num_pages, page_size, max_pages;
+} attn_cache;
+
+/*
+ * Append new tokens: the i-th of row b's counts[b] tokens (NULL: all T)
+ * goes into slot lens[b] + i of every head, K and V from node path[b][i]
+ * (NULL: node i) of k_new, v_new: device bf16 [B][Hkv][T][D] (layouts->k,
+ * layouts->v; NULL contiguous), 16-byte aligned, not overlapping the pools.
+ * positions (device int32 [B][Hkv][capacity], or NULL): the new slots get
+ * seen[b] + i (seen NULL: lens[b] + i), each token's place in the sequence.
+ * lens_out[b] = lens[b] + counts[b]; NULL: the cache's lens are advanced in
+ * place (one more small launch, since every block reads them first).
+ * Tokens beyond the capacity and path entries outside [0, T) are not
+ * written (ATTN_ERR_INDEX); the length stops at the capacity.
+ */
+ATTN25_API int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new, const attn_bf16* v_new,
+                                 int32_t* lens_out, const int32_t* path, const int32_t* counts, int T,
+                                 const attn_layouts* layouts, int32_t* positions, const int32_t* seen,
+                                 attn_stream_t stream);
+
+/*
+ * Attention of new tokens over a cache and over each other: a tree of
+ * drafted tokens (speculative decoding), a chain of them, or a single token.
+ * Query t of row b (t < counts[b]; counts NULL: all T) attends to every
+ * filled slot of its row's cache and, among the row's new tokens, to itself
+ * and its ancestors: parents[b][t] in [-1, t) is t's parent (-1: the cache's
+ * last token), and parents NULL is the chain parents[b][t] = t - 1.
+ *   q, out: device bf16 [B][Hq][T][D]; k_new, v_new: [B][Hkv][T][D] (views
+ *   through layouts: q, k, v, out; NULL contiguous); Hq a multiple of Hkv;
+ *   lse: fp32 [B][Hq][T] contiguous, or NULL; 1 <= T <= 1024.
+ * The new tokens need not be in the cache: they are read from k_new, v_new,
+ * and the accepted ones go in with attn_cache_append.  k_new and v_new both
+ * NULL: the queries see the cache alone (parents must be NULL); a query of a
+ * row with no filled slot then gets O = 0 and LSE = -inf.  Rows t >=
+ * counts[b] of out and lse are left as they were.  A parent outside
+ * [-1, t) counts as -1 (ATTN_ERR_INDEX).
+ * mod_kind: ATTN_MOD_NONE or ATTN_MOD_SOFTCAP (slots of a cache that has
+ * evicted some have no index to mask by; ATTN_ERR_UNSUPPORTED otherwise).
+ * workspace: device memory of at least attn_tree_workspace_size bytes,
+ * 256-byte aligned; its contents on entry do not matter, and calls that
+ * overlap in time need one each.  The result is the same bit for bit on
+ * every run.
+ */
+ATTN25_API size_t attn_tree_workspace_size(int Hq, int Hkv, int T, int D);
+ATTN25_API int attn_tree_fwd(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new,
+                             const attn_cache* cache, attn_bf16* out, float* lse, void* workspace,
+                             size_t workspace_bytes, const int32_t* parents, const int32_t* counts, int Hq,
+                             int T, float scale, int mod_kind, const attn_mod_params* mod_params,
+                             const attn_layouts* layouts, attn_stream_t stream);
+
+/*
+ * The attention weight each slot received: with the row's last counts[b]
+ * (NULL: T) slots holding the tokens whose queries are given,
+ *   weights_out[b][hk][j] = base + sum over the group's query heads h and
+ *       the queries i < counts[b] that see slot j of exp(s'_ij - LSE_i),
+ * where query i (node path[b][i], NULL: i) sees the slots up to its own,
+ * j <= lens[b] - counts[b] + i, s' is the scaled (softcapped) score and
+ * LSE_i = lse[b][h][node], as attn_tree_fwd or attn_fwd (causal, a whole
+ * prompt) wrote it.  base = weights_in[b][hk][j] for the slots before the
+ * row's new ones, 0 for the new ones; weights_in NULL: 0 everywhere.
+ *   q: device bf16 [B][Hq][T][D] (layouts->q); lse: fp32 [B][Hq][T];
+ *   weights_in, weights_out: fp32 [B][Hkv][capacity], which may be the same
+ *   array; entries behind lens[b] are left as they were.  1 <= T <= 262144.
+ * Sums are formed in fp32 in a fixed order.  mod_kind as in attn_tree_fwd.
+ * counts[b] is clamped to lens[b]; path entries outside [0, T) count for
+ * nothing (both ATTN_ERR_INDEX).
+ */
+ATTN25_API int attn_cache_weights(const attn_bf16* q, const float* lse, const attn_cache* cache,
+                                  const float* weights_in, float* weights_out, const int32_t* path,
+                                  const int32_t* counts, int Hq, int T, float scale, int mod_kind,
+                                  const attn_mod_params* mod_params, const attn_layouts* layouts,
+                                  attn_stream_t stream);
+
+/*
+ * Plan an eviction: per (row, head) with more than `budget` filled slots,
+ * keep the `budget` best of them: first those whose position is below
+ * `first` or at least seen[b] - recent (0 <= first + recent <= budget), then
+ * those of larger weight, ties to the lower slot.  (NaN weights count below
+ * all others.)  Nothing is moved yet: moves[b][hk][i] = (to, from), device
+ * int32 [B][Hkv][budget][2] (8-byte aligned), lists the evicted slots below
+ * `budget` and, to fill them, the kept slots from `budget` on, both
+ * ascending; entries from n_moves[b][hk] on are (-1, -1).  weights, positions:
+ * [B][Hkv][capacity]; seen: device int32 [B], tokens so far (one more than
+ * the newest position).  Only the cache's lens and sizes are read.
+ */
+ATTN25_API int attn_evict_plan(const attn_cache* cache, const float* weights, const int32_t* positions,
+                               const int32_t* seen, int32_t* moves, int32_t* n_moves, int budget, int first,
+                               int recent, attn_stream_t stream);
+
+/*
+ * Carry the moves out: rows of K and V, and, where given, entries of weights
+ * and positions, are copied from slot `from` to slot `to`, and lens[b]
+ * becomes min(lens[b], budget).  Slots of a row then hold its tokens in no
+ * particular order, which attention does not mind; positions keep their
+ * places.  moves may come from attn_evict_plan or be the caller's own
+ * (any policy): within a (row, head) the `to` slots must be distinct and no
+ * slot both read and written.  A move outside [0, capacity) is left out
+ * (ATTN_ERR_INDEX).
+ */
+ATTN25_API int attn_cache_compact(const attn_cache* cache, const int32_t* moves, const int32_t* n_moves,
+                                  int budget, float* weights, int32_t* positions, attn_stream_t stream);
 
 /* Synchronise the stream, then return and clear the device status word. */
 ATTN25_API int attn_get_status(attn_stream_t stream);

@@ -31,6 +31,7 @@ from .attention import (  # noqa: F401
     useful_flops,
 )
 from .block_sparsity import block_mask, classify_tiles  # noqa: F401
+from . import cache  # noqa: F401
 from .fp8 import (  # noqa: F401
     attention_forward_fp8,
     fwht,

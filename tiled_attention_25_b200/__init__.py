@@ -9,6 +9,7 @@ from __future__ import annotations
 import torch
 
 from .abi import (  # noqa: F401
+    ATTN_ERR_INDEX,
     ATTN_ERR_TIMEOUT,
     EXPORTED,
     LIB,
@@ -28,6 +29,7 @@ from .abi import (  # noqa: F401
     WALK_CLUSTER_LAUNCH_CONTROL,
     WALK_DEFAULT,
     WALK_STATIC,
+    AttnCache,
     AttnError,
     BlockMask,
     ModParams,
@@ -40,7 +42,11 @@ from .abi import (  # noqa: F401
     attn_bwd_noalloc,
     attn_bwd_noalloc_max_workspace,
     attn_bwd_workspace_size,
+    attn_cache_append,
+    attn_cache_compact,
+    attn_cache_weights,
     attn_check_wait_timeout,
+    attn_evict_plan,
     attn_fp8_rotate_quantize,
     attn_fwd,
     attn_fwd_fp8,
@@ -49,6 +55,8 @@ from .abi import (  # noqa: F401
     attn_set_wait_limit_ms,
     attn_set_work_walk,
     attn_strerror,
+    attn_tree_fwd,
+    attn_tree_workspace_size,
     build_block_mask,
 )
 from .counts import useful_elements, useful_flops  # noqa: F401
@@ -69,6 +77,24 @@ def new_bwd_workspace(B, Hq, Sq, D, device="cuda", deterministic=False) -> torch
     """A 256-byte-aligned workspace of attn_bwd_workspace_size bytes (or, with
     deterministic=True, attn_bwd_deterministic_workspace_size bytes)."""
     nbytes = (attn_bwd_deterministic_workspace_size if deterministic else attn_bwd_workspace_size)(B, Hq, Sq, D)
+    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + nbytes]
+
+
+def new_attn_cache(B, Hkv, capacity, D, page_size=64, device="cuda") -> AttnCache:
+    """An empty cache of `capacity` slots a row (rounded up to whole pages),
+    each row with pages of its own."""
+    pages = -(-capacity // page_size)
+    pool = lambda: torch.empty(B * pages, Hkv, page_size, D, dtype=torch.bfloat16, device=device)  # noqa: E731
+    lens = torch.zeros(B, dtype=torch.int32, device=device)
+    return AttnCache(pool(), pool(), lens)
+
+
+def new_tree_workspace(Hq, Hkv, T, D, device="cuda") -> torch.Tensor:
+    """A 256-byte-aligned workspace of attn_tree_workspace_size bytes (good
+    for every call of up to T tokens with these heads)."""
+    nbytes = attn_tree_workspace_size(Hq, Hkv, T, D)
     buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % 256
     return buf[off:off + nbytes]

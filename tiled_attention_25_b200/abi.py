@@ -34,6 +34,7 @@ MASK_BITMAP = 0x800
 MASK_VARLEN = 0x1000
 
 ATTN_ERR_TIMEOUT = -6
+ATTN_ERR_INDEX = -8
 
 
 class AttnError(RuntimeError):
@@ -88,6 +89,23 @@ class CBlockMask(ctypes.Structure):
     ]
 
 
+class CCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_strides", CStrides),
+        ("v_strides", CStrides),
+        ("page_table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("B", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python tiled_attention_25_b200/build.py`")
@@ -121,6 +139,18 @@ def _load():
     lib.attn_fwd_fp8.restype = I
     lib.attn_fp8_rotate_quantize.argtypes = [P, P, P, P, I, I, I, I, P]
     lib.attn_fp8_rotate_quantize.restype = I
+    lib.attn_cache_append.argtypes = [P, P, P, P, P, P, I, P, P, P, P]
+    lib.attn_cache_append.restype = I
+    lib.attn_tree_workspace_size.argtypes = [I, I, I, I]
+    lib.attn_tree_workspace_size.restype = S
+    lib.attn_tree_fwd.argtypes = [P, P, P, P, P, P, P, S, P, P, I, I, F, I, P, P, P]
+    lib.attn_tree_fwd.restype = I
+    lib.attn_cache_weights.argtypes = [P, P, P, P, P, P, P, I, I, F, I, P, P, P]
+    lib.attn_cache_weights.restype = I
+    lib.attn_evict_plan.argtypes = [P, P, P, P, P, P, I, I, I, P]
+    lib.attn_evict_plan.restype = I
+    lib.attn_cache_compact.argtypes = [P, P, P, I, P, P, P]
+    lib.attn_cache_compact.restype = I
     lib.attn_get_status.argtypes = [P]
     lib.attn_get_status.restype = I
     lib.attn_set_wait_limit_ms.argtypes = [ctypes.c_uint32]
@@ -148,7 +178,9 @@ EXPORTED = ("attn_fwd", "attn_bwd", "attn_bwd_workspace_size", "attn_bwd_noalloc
             "attn_block_mask_bind", "build_block_mask", "attn_get_status",
             "attn_set_wait_limit_ms", "attn_strerror", "attn_fwd_strided", "attn_bwd_strided",
             "attn_bwd_deterministic", "attn_bwd_deterministic_workspace_size", "attn_check_wait_timeout",
-            "attn_fp8_rotate_quantize", "attn_fwd_fp8", "attn_set_work_walk")
+            "attn_fp8_rotate_quantize", "attn_fwd_fp8", "attn_set_work_walk", "attn_cache_append",
+            "attn_tree_workspace_size", "attn_tree_fwd", "attn_cache_weights", "attn_evict_plan",
+            "attn_cache_compact")
 
 
 def attn_strerror(code: int) -> str:
@@ -466,6 +498,152 @@ def build_block_mask(mod_kind, mod_params, B, Sq, Skv, mask: BlockMask, stream=N
     rc = LIB.build_block_mask(int(mod_kind), None if mp is None else mp[0], B, Sq, Skv,
                               ctypes.byref(mask.c), _stream(stream))
     _check(rc, "build_block_mask")
+
+
+class AttnCache:
+    """A paged KV cache: the C struct plus the tensors it points at (kept
+    alive here).  k, v: CUDA bf16 [pages][Hkv][page_size][D] views with their
+    last dimension contiguous; lens: int32 [B]; page_table: int32
+    [B][pages of a row], or None for pages b * n, b * n + 1, ... of row b
+    (n = pages / B)."""
+
+    def __init__(self, k, v, lens, page_table=None):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [pages][Hkv][page_size][D] pools of one shape")
+        self.device = k.device
+        P, Hkv, page, D = k.shape
+        B = lens.shape[0] if lens.dim() == 1 else 0
+        self._own(lens, torch.int32, (B,), "lens")
+        if page_table is None:
+            if B == 0 or P % B:
+                raise ValueError("without a page table the pages must divide evenly among the rows")
+            n = P // B
+        else:
+            n = page_table.shape[-1]
+            self._own(page_table, torch.int32, (B, n), "page_table")
+        self.k, self.v, self.lens, self.page_table = k, v, lens, page_table
+        self.B, self.Hkv, self.D, self.capacity = B, Hkv, D, n * page
+        self.c = CCache(k.data_ptr(), v.data_ptr(), _strides(k, k.shape, "k"), _strides(v, k.shape, "v"),
+                        None if page_table is None else page_table.data_ptr(), lens.data_ptr(), B, Hkv, D, P, page, n)
+        self._own(k, torch.bfloat16, None, "k")
+        self._own(v, torch.bfloat16, None, "v")
+
+    def _own(self, t, dtype, shape, what):
+        """An argument's type, device and (where given) shape and contiguity;
+        its pointer (None stays None)."""
+        if t is None:
+            return None
+        if t.dtype != dtype or t.device != self.device or not t.is_cuda:
+            raise ValueError(f"{what} must be a {dtype} tensor on the cache's CUDA device")
+        if shape is not None and (t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor")
+        return t.data_ptr()
+
+    def _view(self, t, shape, what):
+        """A bf16 [B][H][S][D] view on the cache's device: its pointer and strides."""
+        if t.device != self.device:
+            raise ValueError(f"{what} must be on the cache's device")
+        return t.data_ptr(), _strides(t, shape, what)
+
+    def _call(self, name, stream, *args):
+        """The C call with the cache's device current, on `stream` (default:
+        that device's current stream)."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        fn = getattr(LIB, name)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, _stream(stream))
+        if rc != 0:
+            raise AttnError(rc, name)
+
+
+def _softcap(mod_params):
+    return None if mod_params is None else ctypes.byref(mod_params.c())
+
+
+def attn_cache_append(cache: AttnCache, k_new, v_new, lens_out=None, path=None, counts=None, positions=None, seen=None,
+                      stream=None):
+    """Append (chosen) new K and V rows to the cache (see include/attn25.h).
+    k_new, v_new: bf16 [B][Hkv][T][D] views; path: int32 [B][T]; counts,
+    seen, lens_out: int32 [B]; positions: int32 [B][Hkv][capacity]."""
+    B, T, own = cache.B, k_new.shape[2], cache._own
+    shape = (B, cache.Hkv, T, cache.D)
+    lay = CLayouts()
+    k_ptr, lay.k = cache._view(k_new, shape, "k_new")
+    v_ptr, lay.v = cache._view(v_new, shape, "v_new")
+    i32 = torch.int32
+    cache._call("attn_cache_append", stream, ctypes.byref(cache.c), k_ptr, v_ptr, own(lens_out, i32, (B,), "lens_out"),
+                own(path, i32, (B, T), "path"), own(counts, i32, (B,), "counts"), T, ctypes.byref(lay),
+                own(positions, i32, (B, cache.Hkv, cache.capacity), "positions"), own(seen, i32, (B,), "seen"))
+
+
+def attn_tree_workspace_size(Hq, Hkv, T, D) -> int:
+    return int(LIB.attn_tree_workspace_size(Hq, Hkv, T, D))
+
+
+def attn_tree_fwd(q, k_new, v_new, cache: AttnCache, out, lse, workspace, parents=None, counts=None, scale=None,
+                  mod_kind=MOD_NONE, mod_params=None, stream=None):
+    """Attention of new tokens (a tree, a chain, a single one) over the cache
+    and their own ancestors (see include/attn25.h).  q, out: bf16
+    [B][Hq][T][D] views; k_new, v_new: [B][Hkv][T][D] views, or None both;
+    lse: fp32 [B][Hq][T] or None; parents: int32 [B][T]; counts: int32 [B]."""
+    _, Hq, T, D = q.shape
+    B, own = cache.B, cache._own
+    shape, kv_shape = (B, Hq, T, cache.D), (B, cache.Hkv, T, cache.D)
+    lay = CLayouts()
+    q_ptr, lay.q = cache._view(q, shape, "q")
+    o_ptr, lay.out = cache._view(out, shape, "out")
+    k_ptr = v_ptr = None
+    if k_new is not None:
+        k_ptr, lay.k = cache._view(k_new, kv_shape, "k_new")
+    if v_new is not None:
+        v_ptr, lay.v = cache._view(v_new, kv_shape, "v_new")
+    cache._call("attn_tree_fwd", stream, q_ptr, k_ptr, v_ptr, ctypes.byref(cache.c), o_ptr,
+                own(lse, torch.float32, (B, Hq, T), "lse"), own(workspace, torch.uint8, None, "workspace"),
+                workspace.numel(), own(parents, torch.int32, (B, T), "parents"),
+                own(counts, torch.int32, (B,), "counts"), Hq, T, D ** -0.5 if scale is None else float(scale),
+                int(mod_kind), _softcap(mod_params), ctypes.byref(lay))
+
+
+def attn_cache_weights(q, lse, cache: AttnCache, weights_in, weights_out, path=None, counts=None, scale=None,
+                       mod_kind=MOD_NONE, mod_params=None, stream=None):
+    """Add the attention weight each cached slot received (see
+    include/attn25.h).  q: bf16 [B][Hq][T][D] view; lse: fp32 [B][Hq][T];
+    weights_in (or None), weights_out: fp32 [B][Hkv][capacity]; path: int32
+    [B][T]; counts: int32 [B]."""
+    _, Hq, T, D = q.shape
+    B, own, f32 = cache.B, cache._own, torch.float32
+    lay = CLayouts()
+    q_ptr, lay.q = cache._view(q, (B, Hq, T, cache.D), "q")
+    shape = (B, cache.Hkv, cache.capacity)
+    cache._call("attn_cache_weights", stream, q_ptr, own(lse, f32, (B, Hq, T), "lse"), ctypes.byref(cache.c),
+                own(weights_in, f32, shape, "weights_in"), own(weights_out, f32, shape, "weights_out"),
+                own(path, torch.int32, (B, T), "path"), own(counts, torch.int32, (B,), "counts"), Hq, T,
+                D ** -0.5 if scale is None else float(scale), int(mod_kind), _softcap(mod_params), ctypes.byref(lay))
+
+
+def attn_evict_plan(cache: AttnCache, weights, positions, seen, moves, n_moves, budget, first=0, recent=0, stream=None):
+    """Plan which slots to evict (see include/attn25.h).  weights: fp32,
+    positions: int32, both [B][Hkv][capacity]; seen: int32 [B]; moves: int32
+    [B][Hkv][budget][2]; n_moves: int32 [B][Hkv]."""
+    B, H, own, i32 = cache.B, cache.Hkv, cache._own, torch.int32
+    shape = (B, H, cache.capacity)
+    cache._call("attn_evict_plan", stream, ctypes.byref(cache.c), own(weights, torch.float32, shape, "weights"),
+                own(positions, i32, shape, "positions"), own(seen, i32, (B,), "seen"),
+                own(moves, i32, (B, H, budget, 2), "moves"), own(n_moves, i32, (B, H), "n_moves"), int(budget),
+                int(first), int(recent))
+
+
+def attn_cache_compact(cache: AttnCache, moves, n_moves, budget, weights=None, positions=None, stream=None):
+    """Carry an eviction's moves out (see include/attn25.h)."""
+    B, H, own, i32 = cache.B, cache.Hkv, cache._own, torch.int32
+    shape = (B, H, cache.capacity)
+    cache._call("attn_cache_compact", stream, ctypes.byref(cache.c), own(moves, i32, (B, H, budget, 2), "moves"),
+                own(n_moves, i32, (B, H), "n_moves"), int(budget), own(weights, torch.float32, shape, "weights"),
+                own(positions, i32, shape, "positions"))
 
 
 def attn_get_status(stream=None) -> int:

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "api_common.h"
 #include "attn25.h"
 #include "kernel_common.cuh"
 #include "launch.h"
@@ -38,18 +39,11 @@ std::atomic<int> g_work_walk{1};  // ATTN_WALK_CLUSTER_LAUNCH_CONTROL (default) 
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-  bool ready = false;
-  bool usable = false;
-  int sms = 0;
-  int* status = nullptr;
-  unsigned long long* trace = nullptr;
-  void* scratch = nullptr;  // device address of g_bwd_scratch (nullptr if unavailable)
-};
-
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
 
 int current_device(DeviceInfo** out) {
   int dev = -1;
@@ -88,9 +82,7 @@ int current_device(DeviceInfo** out) {
   return ATTN_OK;
 }
 
-// bf16 tensor [outer][rows][inner] with rows x 64-column boxes, 128-byte swizzle.
-// A [B][H][S][D] bf16 tensor whose D elements are contiguous, as the 4-D map
-// (D, S, H, B) with the tensor's own strides; boxes of 64 x box_rows x 1 x 1.
+// bf16 tensor with rows x 64-column boxes, 128-byte swizzle.
 bool encode_bf16_4d(CUtensorMap* m, const void* base, int D, int S, int H, int B, const Strides& st,
                     int box_rows) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(H),
@@ -103,6 +95,8 @@ bool encode_bf16_4d(CUtensorMap* m, const void* base, int D, int S, int H, int B
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // Contiguous [B][H][S][D = 128] e4m3 codes as the 4-D map (D, S, H, B): one
 // box of 128 bytes x box_rows rows, 128-byte swizzle.
@@ -118,7 +112,8 @@ bool encode_u8_4d(CUtensorMap* m, const void* base, int D, int S, int H, int B, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The strides of a tensor: the caller's, or those of contiguous [B][H][S][D].
+}  // namespace
+
 bool layout_of(const attn_strides* given, int H, int S, int D, Strides& st) {
   if (given == nullptr) {
     st = Strides{static_cast<long long>(H) * S * D, static_cast<long long>(S) * D, D};
@@ -129,11 +124,9 @@ bool layout_of(const attn_strides* given, int H, int S, int D, Strides& st) {
   return st.b >= 8 && st.h >= 8 && st.s >= 8 && st.b % 8 == 0 && st.h % 8 == 0 && st.s % 8 == 0;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-inline int cdiv(int a, int b) { return (a + b - 1) / b; }
-
 uint64_t wait_ns() { return static_cast<uint64_t>(g_wait_ms.load()) * 1000000ull; }
+
+namespace {
 
 // One warp waits, with the kernels' bounded wait, on a barrier that nothing
 // arrives at: after the wait limit it records ATTN_ERR_TIMEOUT in the status
@@ -151,14 +144,7 @@ __global__ void wait_check_kernel(uint64_t limit_ns, int* status) {
   (void)mbar_wait_warp(smem_u32(&bar), 0, wc);
 }
 
-// A mod code split into its score transform and mask bits (composition:
-// one of the seven kinds, optionally ORed with ATTN_MASK_* flags).
-struct ModSpec {
-  int score;      // MOD_NONE, MOD_ALIBI, MOD_SOFTCAP or MOD_BOOST
-  int mask;       // kMask* bits; window and document imply causal
-  int key;        // kernel specialisation key
-  int canonical;  // score | ATTN_MASK_* flags: equal for codes that mean the same mod
-};
+}  // namespace
 
 bool split_mod(int code, ModSpec& m) {
   const int base = code & 0xFF, flags = code & ~0xFF;
@@ -195,6 +181,8 @@ bool split_mod(int code, ModSpec& m) {
                 ((m.mask & kMaskVarlen) ? ATTN_MASK_VARLEN : 0);
   return true;
 }
+
+namespace {
 
 // Shared validation of shapes, mod and mask.
 int check_common(int B, int Hq, int Hkv, int Sq, int Skv, int D, float scale, int mod_kind,
@@ -304,8 +292,6 @@ int mod_key(int mod_kind) {
   return ms.key;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
 struct MaskLayout {
   size_t off[7];
   size_t total;
@@ -343,6 +329,7 @@ const char* attn_strerror(int status) {
     case ATTN_ERR_LAUNCH: return "CUDA launch failed";
     case ATTN_ERR_TIMEOUT: return "kernel timed out waiting on an internal barrier";
     case ATTN_ERR_DEVICE: return "no usable sm_100 device";
+    case ATTN_ERR_INDEX: return "index in a device array out of its bounds";
     default: return "unknown status";
   }
 }

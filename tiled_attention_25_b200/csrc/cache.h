@@ -1,0 +1,94 @@
+// Argument blocks and launchers of the KV-cache kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "cache_index.h"
+#include "launch.h"
+
+namespace attn25 {
+
+constexpr int kErrIndex = -8;
+
+struct CacheDev {
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  Strides k_st, v_st;  // page, head, row
+  CacheIndex ix;
+  int D;
+  int* status;
+};
+
+struct AppendArgs {
+  CacheDev c;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  Strides kn_st, vn_st;
+  const int32_t* path;
+  const int32_t* counts;
+  const int32_t* seen;
+  int32_t* positions;
+  int32_t* lens;      // the cache's own lens (advanced in place when lens_out is nullptr)
+  int32_t* lens_out;
+  int T;
+};
+
+struct TreeArgs {
+  CacheDev c;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_new;  // nullptr: the cache alone
+  const __nv_bfloat16* v_new;
+  Strides q_st, kn_st, vn_st, o_st;
+  __nv_bfloat16* out;
+  float* lse;  // or nullptr
+  const int32_t* parents;
+  const int32_t* counts;
+  int Hq, G, T;
+  float scale, softcap;  // softcap 0: none
+};
+
+struct WeightsArgs {
+  CacheDev c;
+  const __nv_bfloat16* q;
+  Strides q_st;
+  const float* lse;
+  const float* w_in;
+  float* w_out;
+  const int32_t* path;
+  const int32_t* counts;
+  int Hq, G, T;
+  float scale, softcap;
+};
+
+struct PlanArgs {
+  CacheIndex ix;
+  const float* weights;
+  const int32_t* positions;
+  const int32_t* seen;
+  int32_t* moves;
+  int32_t* n_moves;
+  int budget, first, recent;
+  int* status;
+};
+
+struct CompactArgs {
+  CacheDev c;
+  const int32_t* moves;
+  const int32_t* n_moves;
+  float* weights;
+  int32_t* positions;
+  int32_t* lens;
+  int budget;
+};
+
+cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_evict_plan(const PlanArgs& a, cudaStream_t stream);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t stream);
+
+}  // namespace attn25
