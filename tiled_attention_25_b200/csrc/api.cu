@@ -82,18 +82,20 @@ int current_device(DeviceInfo** out) {
   return ATTN_OK;
 }
 
-// bf16 tensor with rows x 64-column boxes, 128-byte swizzle.
-bool encode_bf16_4d(CUtensorMap* m, const void* base, int D, int S, int H, int B, const Strides& st,
-                    int box_rows) {
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(H),
-                        static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.s) * 2, static_cast<cuuint64_t>(st.h) * 2,
-                           static_cast<cuuint64_t>(st.b) * 2};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+bool encode_bf16_dims(CUtensorMap* m, const void* base, const long long (&dims)[4], const long long (&strides)[3],
+                      int box1, int box2) {
+  cuuint64_t d[4], st[3];
+  for (int i = 0; i < 4; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
+  for (int i = 0; i < 3; ++i) st[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_bf16_4d(CUtensorMap* m, const void* base, int D, int S, int H, int B, const Strides& st, int box_rows) {
+  return encode_bf16_dims(m, base, {D, S, H, B}, {st.s, st.h, st.b}, box_rows, 1);
 }
 
 namespace {

@@ -29,6 +29,11 @@ int current_device(DeviceInfo** out);
 // (D, S, H, B) with the tensor's own strides; boxes of 64 x box_rows x 1 x 1.
 bool encode_bf16_4d(CUtensorMap* m, const void* base, int D, int S, int H, int B, const Strides& st, int box_rows);
 
+// Any 4-D bf16 view, dims and boxes innermost first, dim 0 contiguous, element
+// strides of dims 1 to 3; 64-column boxes with the 128-byte swizzle.
+bool encode_bf16_dims(CUtensorMap* m, const void* base, const long long (&dims)[4], const long long (&strides)[3],
+                      int box1, int box2);
+
 // The strides of a tensor: the caller's, or those of contiguous [B][H][S][D];
 // false if a stride is not a positive multiple of 8 elements.
 bool layout_of(const attn_strides* given, int H, int S, int D, Strides& st);

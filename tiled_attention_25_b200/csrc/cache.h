@@ -88,7 +88,15 @@ struct CompactArgs {
 cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_evict_plan(const PlanArgs& a, cudaStream_t stream);
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+// TMA maps of a tree call: q as (D, head, token, row) with boxes of one query
+// tile; the pools as (D, row of the page, head, page) with boxes of
+// min(page_size, 128) rows; k_new and v_new as (D, token, head, row) with
+// boxes of 128 tokens.
+struct TreeMaps {
+  CUtensorMap q, k, v, kn, vn;
+};
+size_t tree_workspace_bytes(int G, int T, int D);
+cudaError_t launch_tree(const TreeMaps& m, const TreeArgs& a, void* workspace, uint64_t wait_ns, cudaStream_t stream);
 cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t stream);
 
 }  // namespace attn25

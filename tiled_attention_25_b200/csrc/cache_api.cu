@@ -110,7 +110,7 @@ int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new, const att
 
 size_t attn_tree_workspace_size(int Hq, int Hkv, int T, int D) {
   if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 1 || T > kMaxTreeTokens || (D != 64 && D != 128)) return 0;
-  return 256;
+  return tree_workspace_bytes(Hq / Hkv, T, D);
 }
 
 int attn_tree_fwd(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new, const attn_cache* cache,
@@ -149,7 +149,17 @@ int attn_tree_fwd(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v
   a.G = Hq / cache->Hkv;
   a.T = T;
   a.scale = scale;
-  return launched(launch_tree(a, reinterpret_cast<cudaStream_t>(stream)));
+  TreeMaps m{};
+  const RowTiles rt = row_tiles(a.G, T);
+  const int box = cache->page_size < TILE ? cache->page_size : TILE;
+  if (!encode_bf16_dims(&m.q, q, {cache->D, Hq, T, cache->B}, {a.q_st.h, a.q_st.s, a.q_st.b}, rt.head_tile, rt.tok_tile) ||
+      !encode_bf16_4d(&m.k, cache->k, cache->D, cache->page_size, cache->Hkv, cache->num_pages, a.c.k_st, box) ||
+      !encode_bf16_4d(&m.v, cache->v, cache->D, cache->page_size, cache->Hkv, cache->num_pages, a.c.v_st, box))
+    return ATTN_ERR_ARG;
+  if (k_new != nullptr && (!encode_bf16_4d(&m.kn, k_new, cache->D, T, cache->Hkv, cache->B, a.kn_st, TILE) ||
+                           !encode_bf16_4d(&m.vn, v_new, cache->D, T, cache->Hkv, cache->B, a.vn_st, TILE)))
+    return ATTN_ERR_ARG;
+  return launched(launch_tree(m, a, workspace, wait_ns(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int attn_cache_weights(const attn_bf16* q, const float* lse, const attn_cache* cache, const float* weights_in,
