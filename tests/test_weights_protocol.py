@@ -1,0 +1,166 @@
+"""A model of cache_weights_kernel's mbarrier protocol, run under random
+interleavings of its warp roles (CPU only).
+
+Roles as in ``tiled_attention_25_b200/csrc/weights_sm100.cu``: the TMA warp
+publishes units and loads K pairs and Q tiles; the column warps fill in each Q
+slot's LSE and limits (one arrival here); the MMA warp forms the scores of one
+or two key tiles per Q tile into two buffers each; two warpgroups sum them.  A
+Q tile may stay for the next unit, and a unit may have no queries.
+
+Checks: no deadlock, no aliasing, and with any one wait of any role running
+out, every role ends with no copy or product in flight.
+"""
+import pytest
+
+from protocol_sim import Sim
+
+
+def roles(sim, units, kbufs, qslots, gathered=False):
+    """units: (Q tiles, key tiles, new_q, keep_q)."""
+    full, empty, drain = sim.full, sim.empty, sim.drain
+    for i in range(2):
+        sim.bar(f"unit_full{i}", 1)
+        sim.bar(f"unit_empty{i}", 4)
+        for t in range(2):
+            sim.bar(f"s_full{t}{i}", 1)
+            sim.bar(f"s_empty{t}{i}", 1)
+    for i in range(kbufs):
+        sim.bar(f"k_full{i}", 1)
+        sim.bar(f"k_empty{i}", 1)
+    for i in range(qslots):
+        sim.bar(f"q_full{i}", 1)
+        sim.bar(f"c_full{i}", 1)
+        sim.bar(f"q_empty{i}", 3)
+    sim.bar("drain", 1)
+    walk = list(units) + [None]
+
+    def tma():
+        kn = ql = 0
+
+        def body():
+            nonlocal kn, ql
+            for it, u in enumerate(walk):
+                if not (yield empty(f"unit_empty{it & 1}", it >> 1)):
+                    return
+                sim.arrive(f"unit_full{it & 1}")
+                if u is None:
+                    return
+                n, _, new, _ = u
+                if n:
+                    if not (yield empty(f"k_empty{kn % kbufs}", kn // kbufs)):
+                        return
+                    sim.load(f"k_full{kn % kbufs}")
+                    kn += 1
+                for _ in range(0 if new else 1, 0 if gathered else n):
+                    if not (yield empty(f"q_empty{ql % qslots}", ql // qslots)):
+                        return
+                    sim.load(f"q_full{ql % qslots}")
+                    ql += 1
+        yield from body()
+        for s in range(kbufs):
+            if (uses := (kn + kbufs - 1 - s) // kbufs):
+                yield drain(f"k_full{s}", uses - 1)
+        for s in range(qslots):
+            if (uses := (ql + qslots - 1 - s) // qslots):
+                yield drain(f"q_full{s}", uses - 1)
+
+    def columns():
+        ql = 0
+        for it, u in enumerate(walk):
+            if not (yield full(f"unit_full{it & 1}", it >> 1)):
+                return
+            sim.arrive(f"unit_empty{it & 1}")
+            if u is None:
+                return
+            for _ in range(0 if u[2] else 1, u[0]):
+                if not (yield empty(f"q_empty{ql % qslots}", ql // qslots)):
+                    return
+                sim.arrive(f"c_full{ql % qslots}")
+                ql += 1
+
+    def mma():
+        def body():
+            kn, ql, sc = 0, 0, [0, 0]
+            for it, u in enumerate(walk):
+                if not (yield full(f"unit_full{it & 1}", it >> 1)):
+                    return
+                sim.arrive(f"unit_empty{it & 1}")
+                if u is None:
+                    return
+                n, tiles, new, keep = u
+                if n == 0:
+                    continue
+                if not (yield full(f"k_full{kn % kbufs}", kn // kbufs)):
+                    return
+                for j in range(n):
+                    ql += j > 0 or new
+                    if not (yield full(f"c_full{(ql - 1) % qslots}", (ql - 1) // qslots)):
+                        return
+                    if not gathered and not (yield full(f"q_full{(ql - 1) % qslots}", (ql - 1) // qslots)):
+                        return
+                    for t in range(tiles):
+                        if not (yield empty(f"s_empty{t}{sc[t] & 1}", sc[t] >> 1)):
+                            return
+                        sim.commit(f"s_full{t}{sc[t] & 1}")
+                        sc[t] += 1
+                    if j < n - 1 or not keep:
+                        sim.commit(f"q_empty{(ql - 1) % qslots}")
+                sim.commit(f"k_empty{kn % kbufs}")
+                kn += 1
+        yield from body()
+        sim.commit("drain")
+        yield drain("drain", 0)
+
+    def sums(t):
+        ql = sc = 0
+        for it, u in enumerate(walk):
+            if not (yield full(f"unit_full{it & 1}", it >> 1)):
+                return
+            sim.arrive(f"unit_empty{it & 1}")
+            if u is None:
+                return
+            n, tiles, new, keep = u
+            for j in range(n):
+                ql += j > 0 or new
+                if not (yield full(f"c_full{(ql - 1) % qslots}", (ql - 1) // qslots)):
+                    return
+                if t < tiles:
+                    if not (yield full(f"s_full{t}{sc & 1}", sc >> 1)):
+                        return
+                    sim.arrive(f"s_empty{t}{sc & 1}")
+                    sc += 1
+                if j < n - 1 or not keep:
+                    sim.arrive(f"q_empty{(ql - 1) % qslots}")
+
+    return {"tma": tma(), "columns": columns(), "mma": mma(), "sums0": sums(0), "sums1": sums(1)}
+
+
+UNITS = {
+    "prompt": [(5, 2, 1, 0), (3, 2, 1, 0), (1, 1, 1, 0)],
+    "draft": [(1, 2, 1, 1), (1, 2, 0, 1), (1, 1, 0, 0), (1, 2, 1, 1), (1, 1, 0, 0), (1, 1, 1, 0)],
+    "half": [(6, 1, 1, 0), (1, 1, 1, 0), (4, 2, 1, 0)],
+    "no queries": [(0, 2, 0, 0), (0, 1, 0, 0), (1, 2, 1, 0), (0, 2, 0, 0)],
+    "nothing": [],
+}
+
+
+@pytest.mark.parametrize("gathered", [False, True])
+@pytest.mark.parametrize("bufs", [(2, 2), (4, 4)])
+@pytest.mark.parametrize("name", sorted(UNITS))
+def test_weights_protocol_never_deadlocks_or_aliases(name, bufs, gathered):
+    for seed in range(120):
+        sim = Sim(seed)
+        stuck = sim.run(roles(sim, UNITS[name], *bufs, gathered))
+        assert stuck is None, f"{name}, seed {seed}: {stuck}"
+        assert sim.in_flight_at_exit == 0
+
+
+@pytest.mark.parametrize("role", ["tma", "columns", "mma", "sums0", "sums1"])
+def test_a_wait_that_runs_out_ends_every_role(role):
+    for name in ("prompt", "draft", "half"):
+        for at in range(20):
+            for seed in range(8):
+                sim = Sim(seed)
+                stuck = sim.run(roles(sim, UNITS[name], 2, 2), give_up=(role, at))
+                assert stuck is None, f"{role} wait {at}, seed {seed}: {stuck}"
+                assert sim.in_flight_at_exit == 0, f"{role} wait {at}, seed {seed}: {sim.pending_at_exit}"

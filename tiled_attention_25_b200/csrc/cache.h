@@ -97,6 +97,8 @@ struct TreeMaps {
 };
 size_t tree_workspace_bytes(int G, int T, int D);
 cudaError_t launch_tree(const TreeMaps& m, const TreeArgs& a, void* workspace, uint64_t wait_ns, cudaStream_t stream);
-cudaError_t launch_cache_weights(const WeightsArgs& a, cudaStream_t stream);
+// tq, tk: maps as in TreeMaps
+cudaError_t launch_cache_weights(const CUtensorMap& tq, const CUtensorMap& tk, const WeightsArgs& a, uint64_t wait_ns, int sms,
+                                 cudaStream_t stream);
 
 }  // namespace attn25

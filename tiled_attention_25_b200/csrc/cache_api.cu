@@ -68,6 +68,17 @@ int check_scores(const attn_cache* c, int Hq, float scale, int mod_kind, const a
   return ATTN_OK;
 }
 
+// q as (D, head, token, row), one query tile to a box
+bool encode_query_tiles(CUtensorMap* m, const void* q, const attn_cache* c, int Hq, int T, const Strides& st) {
+  const RowTiles rt = row_tiles(Hq / c->Hkv, T);
+  return encode_bf16_dims(m, q, {c->D, Hq, T, c->B}, {st.h, st.s, st.b}, rt.head_tile, rt.tok_tile);
+}
+
+// a pool as (D, row of the page, head, page), min(page_size, 128) rows to a box
+bool encode_pool(CUtensorMap* m, const void* pool, const attn_cache* c, const Strides& st) {
+  return encode_bf16_4d(m, pool, c->D, c->page_size, c->Hkv, c->num_pages, st, c->page_size < TILE ? c->page_size : TILE);
+}
+
 int launched(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH; }
 
 }  // namespace
@@ -150,11 +161,8 @@ int attn_tree_fwd(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v
   a.T = T;
   a.scale = scale;
   TreeMaps m{};
-  const RowTiles rt = row_tiles(a.G, T);
-  const int box = cache->page_size < TILE ? cache->page_size : TILE;
-  if (!encode_bf16_dims(&m.q, q, {cache->D, Hq, T, cache->B}, {a.q_st.h, a.q_st.s, a.q_st.b}, rt.head_tile, rt.tok_tile) ||
-      !encode_bf16_4d(&m.k, cache->k, cache->D, cache->page_size, cache->Hkv, cache->num_pages, a.c.k_st, box) ||
-      !encode_bf16_4d(&m.v, cache->v, cache->D, cache->page_size, cache->Hkv, cache->num_pages, a.c.v_st, box))
+  if (!encode_query_tiles(&m.q, q, cache, Hq, T, a.q_st) || !encode_pool(&m.k, cache->k, cache, a.c.k_st) ||
+      !encode_pool(&m.v, cache->v, cache, a.c.v_st))
     return ATTN_ERR_ARG;
   if (k_new != nullptr && (!encode_bf16_4d(&m.kn, k_new, cache->D, T, cache->Hkv, cache->B, a.kn_st, TILE) ||
                            !encode_bf16_4d(&m.vn, v_new, cache->D, T, cache->Hkv, cache->B, a.vn_st, TILE)))
@@ -191,7 +199,9 @@ int attn_cache_weights(const attn_bf16* q, const float* lse, const attn_cache* c
   a.G = Hq / cache->Hkv;
   a.T = T;
   a.scale = scale;
-  return launched(launch_cache_weights(a, reinterpret_cast<cudaStream_t>(stream)));
+  CUtensorMap tq, tk;
+  if (!encode_query_tiles(&tq, q, cache, Hq, T, a.q_st) || !encode_pool(&tk, cache->k, cache, a.c.k_st)) return ATTN_ERR_ARG;
+  return launched(launch_cache_weights(tq, tk, a, wait_ns(), d->sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int attn_evict_plan(const attn_cache* cache, const float* weights, const int32_t* positions, const int32_t* seen,
