@@ -232,6 +232,16 @@ def test_plan_long(ta, n, budget):
     plan_check(ta, w, pos, seen, [n, n - 1], pages, budget, 4, budget // 8)
 
 
+def test_plan_many_heads_and_ranks_that_do_not_fit(ta):
+    """More heads than SMs, so one CTA to each, and a row too long for its shared memory; and the full capacity."""
+    lens = [5] * 299 + [60000]
+    w, pos, seen, pages = plan_case(5, lens, 1, 300, 0)
+    plan_check(ta, w, pos, seen, lens, pages, 300, 4, 100)
+    lens = [1 << 20, 100]
+    w, pos, seen, pages = plan_case(6, lens, 1, 5000, 0, page=1 << 14)
+    plan_check(ta, w, pos, seen, lens, pages, 5000, 0, 17, page=1 << 14)
+
+
 def test_plan_strange_weights(ta):
     """Infinities, NaN, zeros of both signs, negative and denormal weights."""
     w, pos, seen, n = plan_case(3, [256, 256], 2, 100, 0)

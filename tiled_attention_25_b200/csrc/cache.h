@@ -73,6 +73,7 @@ struct PlanArgs {
   int32_t* n_moves;
   int budget, first, recent;
   int* status;
+  int mask_words, held_keys;  // words of a share's masks and ranks of it kept in shared memory (set by the launcher)
 };
 
 struct CompactArgs {
@@ -87,7 +88,7 @@ struct CompactArgs {
 
 cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_evict_plan(const PlanArgs& a, cudaStream_t stream);
+cudaError_t launch_evict_plan(const PlanArgs& a, int sms, cudaStream_t stream);
 // TMA maps of a tree call: q as (D, head, token, row) with boxes of one query
 // tile; the pools as (D, row of the page, head, page) with boxes of
 // min(page_size, 128) rows; k_new and v_new as (D, token, head, row) with

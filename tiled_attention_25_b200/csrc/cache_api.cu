@@ -218,8 +218,8 @@ int attn_evict_plan(const attn_cache* cache, const float* weights, const int32_t
   DeviceInfo* d = nullptr;
   rc = current_device(&d);
   if (rc != ATTN_OK) return rc;
-  PlanArgs a{index_of(cache), weights, positions, seen, moves, n_moves, budget, first, recent, d->status};
-  return launched(launch_evict_plan(a, reinterpret_cast<cudaStream_t>(stream)));
+  PlanArgs a{index_of(cache), weights, positions, seen, moves, n_moves, budget, first, recent, d->status, 0, 0};
+  return launched(launch_evict_plan(a, d->sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int attn_cache_compact(const attn_cache* cache, const int32_t* moves, const int32_t* n_moves, int budget,

@@ -12,39 +12,79 @@ namespace {
 
 __device__ __forceinline__ void flag_index(int* status) { atomicCAS(status, 0, kErrIndex); }
 
-// ------------------------------------------------------------------ append
+// ------------------------------------------------------------------ row copies
 //
-// A copy: every new row is read once and written once, 16 bytes a thread.
-// Thread order within a block: 16-byte chunk of the row, K or V, row.
+// Append and compaction are copies of K and V rows, read once and written
+// once, bound by HBM.  A row's place is two dependent lookups away (its token
+// or move, then the page table), so a block first resolves the element offsets
+// of a batch of rows, one thread to a row, into shared memory, and then
+// streams the batch with eight 16-byte loads of a thread in flight.  (With the
+// lookups in every copying thread the halving of 16 x 8 heads of 8192 slots
+// took 94 to 109 us.)
 constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+
+template <int D>
+struct CopyBatch {
+  static constexpr int kChunks = D / 8;                                    // 16-byte chunks of a row
+  static constexpr int kRows = kCopyThreads * kCopyUnroll / (2 * kChunks);  // rows of a batch
+  long long src[2][kRows], dst[2][kRows];  // elements, K and V; src < 0: no copy
+};
+
+// Executed by the block after a __syncthreads.  Thread order: chunk, K or V, row.
+template <int D>
+__device__ __forceinline__ void copy_rows(const CopyBatch<D>& t, const __nv_bfloat16* src_k, const __nv_bfloat16* src_v,
+                                          __nv_bfloat16* dst_k, __nv_bfloat16* dst_v) {
+  using T = CopyBatch<D>;
+  constexpr int kStep = kCopyThreads / (2 * T::kChunks);
+  const int chunk = threadIdx.x % T::kChunks, is_v = threadIdx.x / T::kChunks % 2, r = threadIdx.x / (2 * T::kChunks);
+  const __nv_bfloat16* src = (is_v ? src_v : src_k) + chunk * 8;
+  __nv_bfloat16* dst = (is_v ? dst_v : dst_k) + chunk * 8;
+  uint4 v[kCopyUnroll];
+#pragma unroll
+  for (int x = 0; x < kCopyUnroll; ++x) {
+    const long long at = t.src[is_v][r + x * kStep];
+    if (at >= 0) v[x] = *reinterpret_cast<const uint4*>(src + at);
+  }
+#pragma unroll
+  for (int x = 0; x < kCopyUnroll; ++x)
+    if (t.src[is_v][r + x * kStep] >= 0) *reinterpret_cast<uint4*>(dst + t.dst[is_v][r + x * kStep]) = v[x];
+}
 
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) append_kernel(const AppendArgs a) {
-  constexpr int kChunks = D / 8;                              // 16-byte chunks of a row
-  constexpr int kRows = kCopyThreads / (2 * kChunks);         // rows of a block's pass
+  using T = CopyBatch<D>;
+  __shared__ T t;
   const int b = blockIdx.z, hk = blockIdx.y;
   bool bad = false;
   const int n = a.counts != nullptr ? clamp_count(a.counts[b], a.T, bad) : a.T;
   const int len = clamp_count(a.c.ix.lens[b], a.c.ix.capacity, bad);
-  const int chunk = threadIdx.x % kChunks, is_v = threadIdx.x / kChunks % 2, r = threadIdx.x / (2 * kChunks);
-  for (int i = blockIdx.x * kRows + r; i < n; i += gridDim.x * kRows) {
-    const int slot = len + i, node = a.path != nullptr ? a.path[static_cast<long long>(b) * a.T + i] : i;
-    if (slot >= a.c.ix.capacity || node < 0 || node >= a.T) {
-      bad = true;
-      continue;
+  const int ps = a.c.ix.page_size;
+  for (int i0 = blockIdx.x * T::kRows; i0 < n; i0 += gridDim.x * T::kRows) {
+    if (threadIdx.x < T::kRows) {
+      const int i = i0 + threadIdx.x, slot = len + i;
+      long long from = -1;
+      if (i < n) {
+        const int node = a.path != nullptr ? a.path[static_cast<long long>(b) * a.T + i] : i;
+        if (slot < a.c.ix.capacity && node >= 0 && node < a.T) {
+          if (a.positions != nullptr)
+            a.positions[slot_entry(a.c.ix, b, hk, slot)] = (a.seen != nullptr ? a.seen[b] : len) + i;
+          const int page = page_at(a.c.ix, b, slot / ps), row = slot % ps;
+          if (page >= 0) {
+            from = node;
+            t.dst[0][threadIdx.x] = page * a.c.k_st.b + row * a.c.k_st.s;
+            t.dst[1][threadIdx.x] = page * a.c.v_st.b + row * a.c.v_st.s;
+          }
+        }
+        bad = bad || from < 0;
+      }
+      t.src[0][threadIdx.x] = from < 0 ? -1 : from * a.kn_st.s;
+      t.src[1][threadIdx.x] = from < 0 ? -1 : from * a.vn_st.s;
     }
-    if (a.positions != nullptr && chunk == 0 && is_v == 0)
-      a.positions[slot_entry(a.c.ix, b, hk, slot)] = (a.seen != nullptr ? a.seen[b] : len) + i;
-    const int page = page_at(a.c.ix, b, slot / a.c.ix.page_size), row = slot % a.c.ix.page_size;
-    if (page < 0) {
-      bad = true;
-      continue;
-    }
-    const Strides& from = is_v ? a.vn_st : a.kn_st;
-    const Strides& to = is_v ? a.c.v_st : a.c.k_st;
-    const __nv_bfloat16* src = (is_v ? a.v_new : a.k_new) + b * from.b + hk * from.h + node * from.s + chunk * 8;
-    __nv_bfloat16* dst = (is_v ? a.c.v : a.c.k) + page * to.b + hk * to.h + row * to.s + chunk * 8;
-    *reinterpret_cast<uint4*>(dst) = __ldg(reinterpret_cast<const uint4*>(src));
+    __syncthreads();
+    copy_rows<D>(t, a.k_new + b * a.kn_st.b + hk * a.kn_st.h, a.v_new + b * a.vn_st.b + hk * a.vn_st.h, a.c.k + hk * a.c.k_st.h,
+                 a.c.v + hk * a.c.v_st.h);
+    __syncthreads();
   }
   if (a.lens_out != nullptr && blockIdx.x == 0 && hk == 0 && threadIdx.x == 0)
     a.lens_out[b] = min(len + n, a.c.ix.capacity);
@@ -61,36 +101,41 @@ __global__ void advance_kernel(const AppendArgs a) {
   a.lens[b] = min(len + n, a.c.ix.capacity);
 }
 
-// ------------------------------------------------------------------ compact
-
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const CompactArgs a) {
-  constexpr int kChunks = D / 8;
-  constexpr int kRows = kCopyThreads / (2 * kChunks);
+  using T = CopyBatch<D>;
+  __shared__ T t;
   const int b = blockIdx.y / a.c.ix.Hkv, hk = blockIdx.y % a.c.ix.Hkv;
   bool bad = false;
   const int n = clamp_count(a.n_moves[blockIdx.y], a.budget, bad);
-  const int chunk = threadIdx.x % kChunks, is_v = threadIdx.x / kChunks % 2, r = threadIdx.x / (2 * kChunks);
   const int ps = a.c.ix.page_size;
-  for (int i = blockIdx.x * kRows + r; i < n; i += gridDim.x * kRows) {
-    const int2 mv = reinterpret_cast<const int2*>(a.moves)[static_cast<long long>(blockIdx.y) * a.budget + i];
-    if (mv.x < 0 || mv.x >= a.c.ix.capacity || mv.y < 0 || mv.y >= a.c.ix.capacity) {
-      bad = true;
-      continue;
+  const int2* moves = reinterpret_cast<const int2*>(a.moves) + static_cast<long long>(blockIdx.y) * a.budget;
+  for (int i0 = blockIdx.x * T::kRows; i0 < n; i0 += gridDim.x * T::kRows) {
+    if (threadIdx.x < T::kRows) {
+      const int i = i0 + threadIdx.x;
+      bool moved = false;
+      if (i < n) {
+        const int2 mv = moves[i];
+        if (mv.x >= 0 && mv.x < a.c.ix.capacity && mv.y >= 0 && mv.y < a.c.ix.capacity) {
+          const long long to = slot_entry(a.c.ix, b, hk, mv.x), from = slot_entry(a.c.ix, b, hk, mv.y);
+          if (a.weights != nullptr) a.weights[to] = a.weights[from];
+          if (a.positions != nullptr) a.positions[to] = a.positions[from];
+          const int pt = page_at(a.c.ix, b, mv.x / ps), pf = page_at(a.c.ix, b, mv.y / ps);
+          if (pt >= 0 && pf >= 0) {
+            moved = true;
+            t.dst[0][threadIdx.x] = pt * a.c.k_st.b + mv.x % ps * a.c.k_st.s;
+            t.dst[1][threadIdx.x] = pt * a.c.v_st.b + mv.x % ps * a.c.v_st.s;
+            t.src[0][threadIdx.x] = pf * a.c.k_st.b + mv.y % ps * a.c.k_st.s;
+            t.src[1][threadIdx.x] = pf * a.c.v_st.b + mv.y % ps * a.c.v_st.s;
+          }
+        }
+        bad = bad || !moved;
+      }
+      if (!moved) t.src[0][threadIdx.x] = t.src[1][threadIdx.x] = -1;
     }
-    if (chunk == 0 && is_v == 0 && a.weights != nullptr)
-      a.weights[slot_entry(a.c.ix, b, hk, mv.x)] = a.weights[slot_entry(a.c.ix, b, hk, mv.y)];
-    if (chunk == 0 && is_v == 1 && a.positions != nullptr)
-      a.positions[slot_entry(a.c.ix, b, hk, mv.x)] = a.positions[slot_entry(a.c.ix, b, hk, mv.y)];
-    const int pt = page_at(a.c.ix, b, mv.x / ps), pf = page_at(a.c.ix, b, mv.y / ps);
-    if (pt < 0 || pf < 0) {
-      bad = true;
-      continue;
-    }
-    const Strides& st = is_v ? a.c.v_st : a.c.k_st;
-    __nv_bfloat16* base = (is_v ? a.c.v : a.c.k) + hk * st.h + chunk * 8;
-    *reinterpret_cast<uint4*>(base + pt * st.b + mv.x % ps * st.s) =
-        *reinterpret_cast<const uint4*>(base + pf * st.b + mv.y % ps * st.s);
+    __syncthreads();
+    copy_rows<D>(t, a.c.k + hk * a.c.k_st.h, a.c.v + hk * a.c.v_st.h, a.c.k + hk * a.c.k_st.h, a.c.v + hk * a.c.v_st.h);
+    __syncthreads();
   }
   if (blockIdx.x == 0 && hk == 0 && threadIdx.x == 0) a.lens[b] = min(clamp_count(a.lens[b], a.c.ix.capacity, bad), a.budget);
   if (bad) flag_index(a.c.status);
@@ -107,100 +152,252 @@ __device__ __forceinline__ uint32_t slot_rank(float w, int pos, int first, int r
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kPlanThreads = 1024;
+// One cluster of 1 to 8 CTAs per (row, head), each with an equal share of the
+// slots, whose ranks it keeps in shared memory (read again from global where
+// they do not fit).  A radix select finds the budget-th largest rank in at
+// most three passes of 11, 11 and 10 bits; every CTA adds up the cluster's
+// histograms over distributed shared memory and takes the same decision.  Then
+// each warp walks its part in slot order: ranks of equal ones, kept slots as
+// bit masks, and the places of the holes and of the rows that fill them, from
+// prefix counts over the warps and the CTAs.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kPlanSmem = 227 * 1024;
 
-// Exclusive prefix sum over the block of one count a thread; total in `sum`.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int& sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  int before = 0;
-  sum = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += warp_sums[w];
-    sum += warp_sums[w];
-  }
-  __syncthreads();
-  return before + inc - x;
+struct PlanShared {
+  int hist[3][kBins];
+  int warp_sum[kPlanWarps];
+  int tie_warp[kPlanWarps], hole_warp[kPlanWarps], extra_warp[kPlanWarps];
+  int ties, holes, extras;  // of this CTA, read by the cluster
+  uint32_t digit;
+  int need, in_bin;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// The word at `p` of the same shared layout in CTA `rank` of the cluster.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .u32 r;\n\t"
+      "mapa.shared::cluster.u32 r, %1, %2;\n\t"
+      "ld.shared::cluster.s32 %0, [r];\n\t}"
+      : "=r"(v)
+      : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank)
+      : "memory");
+  return v;
 }
 
-// One block per (row, head): a radix select of the budget-th largest rank (8
-// bits a pass), then one pass in slot order that hands the holes below the
-// budget and the kept slots above it their places in the move list.
+// Sum of the counts of the warps before this one.
+__device__ __forceinline__ int warps_before(const int* counts) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = lane < warp && lane < kPlanWarps ? counts[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// Sum of the counts of the CTAs before this one, and of all.
+__device__ __forceinline__ int ctas_before(const int* count, int& all) {
+  int before = 0;
+  all = 0;
+  for (uint32_t c = 0; c < cluster_size(); ++c) {
+    const int v = ld_cluster(count, c);
+    if (c < cluster_rank()) before += v;
+    all += v;
+  }
+  return before;
+}
+
+__device__ __forceinline__ int warp_total(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// One more in a bin of the histogram.  Weights of one size share few bins of
+// the first pass, and atomics on one address take turns, so the lanes of a bin
+// are added up first.
+__device__ __forceinline__ void count(int* hist, uint32_t bin, bool in) {
+  const uint32_t active = __activemask();
+  const uint32_t same = __match_any_sync(active, in ? bin : 0xffffffffu);
+  if (in && static_cast<int>(threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
-  const int bh = blockIdx.x, b = bh / a.ix.Hkv;
+  extern __shared__ __align__(16) uint8_t plan_smem[];
+  PlanShared& sh = *reinterpret_cast<PlanShared*>(plan_smem);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(plan_smem + sizeof(PlanShared));  // kept slots of the share
+  uint32_t* keys = mask + a.mask_words;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t lt = (1u << lane) - 1u;
+  const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int bh = blockIdx.x / ctas, b = bh / a.ix.Hkv;
   bool bad = false;
   const int n = clamp_count(a.ix.lens[b], a.ix.capacity, bad);
   if (bad && threadIdx.x == 0) flag_index(a.status);
   int2* moves = reinterpret_cast<int2*>(a.moves) + static_cast<long long>(bh) * a.budget;
-  __shared__ int hist[256];
-  __shared__ int sums[kPlanThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
   int n_moves = 0;
-  if (n > a.budget) {
+  if (n > a.budget) {  // the same for the whole cluster
     const float* w = a.weights + static_cast<long long>(bh) * a.ix.capacity;
     const int32_t* pos = a.positions + static_cast<long long>(bh) * a.ix.capacity;
     const int recent_from = a.seen[b] - a.recent;
-    uint32_t prefix = 0;
-    int need = a.budget;  // slots still to take among those that share the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kPlanThreads) hist[i] = 0;
+    // this CTA's slots [j0, j0 + m), whole words of the masks
+    const int share = ((n + ctas - 1) / ctas + 31) / 32 * 32;
+    const int j0 = min(n, rank * share), m = min(n - j0, share);
+    const bool held = share <= a.held_keys;
+    auto fresh = [&](int i) { return slot_rank(w[j0 + i], pos[j0 + i], a.first, recent_from); };
+    auto key = [&](int i) { return held ? keys[i] : fresh(i); };
+    for (int i = threadIdx.x; i < 3 * kBins; i += kPlanThreads) (&sh.hist[0][0])[i] = 0;
+    __syncthreads();
+    uint32_t prefix = 0;     // the bits decided so far
+    int need = a.budget;     // slots still to take among those that share them
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
+      const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);  // bits below the decided ones
+      int* hist = sh.hist[pass];
+      if (pass == 0) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < m; i += kPlanThreads) {
+          const uint32_t k = fresh(i);
+          if (held) keys[i] = k;
+          count(hist, k >> shift, true);
+        }
+      } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < m; i += kPlanThreads) {
+          const uint32_t k = key(i);
+          count(hist, (k >> shift) & (bins - 1), (k >> above) == (prefix >> above));
+        }
+      }
+      if (ctas > 1) cluster_sync();
+      else __syncthreads();
+      // the bin in which the count from the top reaches `need`: four bins to a thread, from the top
+      int c[4], sum = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int bin = bins - 1 - (4 * static_cast<int>(threadIdx.x) + x);
+        c[x] = 0;
+        if (bin >= 0) {
+          if (ctas == 1) c[x] = hist[bin];
+          else
+            for (int q = 0; q < ctas; ++q) c[x] += ld_cluster(&hist[bin], q);
+        }
+        sum += c[x];
+      }
+      int inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) sh.warp_sum[warp] = inc;
       __syncthreads();
-      for (int j = threadIdx.x; j < n; j += kPlanThreads) {
-        const uint32_t k = slot_rank(w[j], pos[j], a.first, recent_from);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+      int before = warps_before(sh.warp_sum) + inc - sum;
+      if (before < need && before + sum >= need) {
+        int x = 0;
+        while (before + c[x] < need) before += c[x++];
+        sh.digit = bins - 1 - (4 * threadIdx.x + x);
+        sh.need = need - before;
+        sh.in_bin = c[x];
       }
       __syncthreads();
-      if (threadIdx.x == 0) {
-        int left = need, d = 255;
-        while (d > 0 && hist[d] < left) left -= hist[d--];
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-        s_need = left;
+      prefix |= sh.digit << shift;
+      need = sh.need;
+      if (need == sh.in_bin) {  // the whole bin stays: what is at or above its lowest rank
+        prefix -= 1;            // (something lies below, or n <= budget)
+        need = 0;
+        break;
       }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
-      __syncthreads();
     }
-    // slots of rank above `prefix` stay, and the first `need` of equal rank
-    int ties = 0, holes = 0, extras = 0;
-    for (int j0 = 0; j0 < n; j0 += kPlanThreads) {
-      const int j = j0 + threadIdx.x;
-      const uint32_t k = j < n ? slot_rank(w[j], pos[j], a.first, recent_from) : 0;
-      const int tie = j < n && k == prefix;
-      int sum;
-      const int t = ties + block_scan(tie, sums, sum);
-      ties += sum;
-      const bool keep = j < n && (k > prefix || (tie && t < need));
-      const int hole = j < min(n, a.budget) && !keep, extra = keep && j >= a.budget;
-      // a chunk may hold both sides of the budget: two scans
-      const int at_h = holes + block_scan(hole, sums, sum);
-      holes += sum;
-      const int at_e = extras + block_scan(extra, sums, sum);
-      extras += sum;
-      if (hole) moves[at_h].x = j;
-      if (extra) moves[at_e].y = j;
+    // slots of rank above `prefix` stay, and the first `need` (in slot order) of equal rank
+    const int words = (m + 31) / 32, per = (words + kPlanWarps - 1) / kPlanWarps;
+    const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
+    int t = 0;
+    if (need > 0)
+      for (int x = w0; x < w1; ++x) {
+        const int i = x * 32 + lane;
+        t += i < m && key(i) == prefix;
+      }
+    t = warp_total(t);
+    if (lane == 0) sh.tie_warp[warp] = t;
+    __syncthreads();
+    if (warp == 0) {
+      const int v = warp_total(lane < kPlanWarps ? sh.tie_warp[lane] : 0);
+      if (lane == 0) sh.ties = v;
     }
-    n_moves = holes;
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    int all;
+    int tie = ctas_before(&sh.ties, all) + warps_before(sh.tie_warp);
+    int holes = 0, extras = 0;
+    for (int x = w0; x < w1; ++x) {
+      const int i = x * 32 + lane;
+      const uint32_t k = i < m ? key(i) : 0u;
+      const uint32_t eq = __ballot_sync(0xffffffffu, need > 0 && i < m && k == prefix);
+      const bool keep = i < m && (k > prefix || (((eq >> lane) & 1u) && tie + __popc(eq & lt) < need));
+      tie += __popc(eq);
+      const uint32_t kept = __ballot_sync(0xffffffffu, keep), low = __ballot_sync(0xffffffffu, i < m && j0 + i < a.budget);
+      if (lane == 0) mask[x] = kept;
+      holes += __popc(low & ~kept);
+      extras += __popc(kept & ~low);
+    }
+    if (lane == 0) {
+      sh.hole_warp[warp] = holes;
+      sh.extra_warp[warp] = extras;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int h = warp_total(lane < kPlanWarps ? sh.hole_warp[lane] : 0);
+      const int e = warp_total(lane < kPlanWarps ? sh.extra_warp[lane] : 0);
+      if (lane == 0) {
+        sh.holes = h;
+        sh.extras = e;
+      }
+    }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    int at_h = ctas_before(&sh.holes, n_moves) + warps_before(sh.hole_warp);
+    int at_e = ctas_before(&sh.extras, all) + warps_before(sh.extra_warp);
+    for (int x = w0; x < w1; ++x) {
+      const int j = j0 + x * 32 + lane;
+      const uint32_t kept = mask[x], low = __ballot_sync(0xffffffffu, j < a.budget && j < n);
+      const uint32_t hole = low & ~kept, extra = kept & ~low;
+      if ((hole >> lane) & 1u) moves[at_h + __popc(hole & lt)].x = j;
+      if ((extra >> lane) & 1u) moves[at_e + __popc(extra & lt)].y = j;
+      at_h += __popc(hole);
+      at_e += __popc(extra);
+    }
+    if (ctas > 1) cluster_sync();  // the others may still read this CTA's counts
   }
-  for (int i = n_moves + threadIdx.x; i < a.budget; i += kPlanThreads) moves[i] = make_int2(-1, -1);
-  if (threadIdx.x == 0) a.n_moves[bh] = n_moves;
+  for (int i = n_moves + rank * kPlanThreads + threadIdx.x; i < a.budget; i += ctas * kPlanThreads) moves[i] = make_int2(-1, -1);
+  if (rank == 0 && threadIdx.x == 0) a.n_moves[bh] = n_moves;
 }
 
 }  // namespace
 
+// Blocks to a head: enough for eight to an SM over all heads, each with a batch at least.
+static int copy_blocks(int rows, int batch, long long heads, int sms) {
+  const long long most = (static_cast<long long>(rows) + batch - 1) / batch, want = (8LL * sms + heads - 1) / heads;
+  return static_cast<int>(most < want ? most : want);
+}
+
 cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t stream) {
-  const int rows = kCopyThreads / (2 * a.c.D / 8);
-  const long long heads = static_cast<long long>(a.c.ix.B) * a.c.ix.Hkv;
-  const long long most = (a.T + rows - 1) / rows, want = (8LL * sms + heads - 1) / heads;
-  const dim3 grid(static_cast<unsigned>(most < want ? most : want), a.c.ix.Hkv, a.c.ix.B);
+  const int batch = a.c.D == 128 ? CopyBatch<128>::kRows : CopyBatch<64>::kRows;
+  const dim3 grid(copy_blocks(a.T, batch, static_cast<long long>(a.c.ix.B) * a.c.ix.Hkv, sms), a.c.ix.Hkv, a.c.ix.B);
   if (a.c.D == 128) append_kernel<128><<<grid, kCopyThreads, 0, stream>>>(a);
   else append_kernel<64><<<grid, kCopyThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
@@ -210,18 +407,39 @@ cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t strea
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t stream) {
-  const int rows = kCopyThreads / (2 * a.c.D / 8);
-  const int heads = a.c.ix.B * a.c.ix.Hkv;
-  const int most = (a.budget + rows - 1) / rows, want = (8 * sms + heads - 1) / heads;
-  const dim3 grid(most < want ? most : want, heads);
+  const int batch = a.c.D == 128 ? CopyBatch<128>::kRows : CopyBatch<64>::kRows, heads = a.c.ix.B * a.c.ix.Hkv;
+  const dim3 grid(copy_blocks(a.budget, batch, heads, sms), heads);
   if (a.c.D == 128) compact_kernel<128><<<grid, kCopyThreads, 0, stream>>>(a);
   else compact_kernel<64><<<grid, kCopyThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_evict_plan(const PlanArgs& a, cudaStream_t stream) {
-  plan_kernel<<<a.ix.B * a.ix.Hkv, kPlanThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_evict_plan(const PlanArgs& args, int sms, cudaStream_t stream) {
+  PlanArgs a = args;
+  const int heads = a.ix.B * a.ix.Hkv;
+  // CTAs to a head: more while they do not fill the SMs twice over and every one keeps 2048 slots
+  int ctas = 1;
+  while (ctas < 8 && heads * ctas * 2 <= 2 * sms && a.ix.capacity / (ctas * 2) >= 2048) ctas *= 2;
+  const int share = ((a.ix.capacity + ctas - 1) / ctas + 31) / 32 * 32;
+  a.mask_words = share / 32;
+  const int room = (kPlanSmem - static_cast<int>(sizeof(PlanShared))) / 4 - a.mask_words;
+  a.held_keys = share < room ? share : room;  // a row shorter than the capacity has a smaller share
+  const size_t smem = sizeof(PlanShared) + (static_cast<size_t>(a.mask_words) + a.held_keys) * 4;
+  cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(heads * ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_kernel, a);
 }
 
 }  // namespace attn25
