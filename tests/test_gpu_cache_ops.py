@@ -202,13 +202,17 @@ def plan_case(seed, lens, Hkv, budget, recent, cap=None, ties=0.2, page=64):
     return w, pos, seen, n
 
 
-def plan_check(ta, w, pos, seen, lens, n, budget, first, recent, page=64):
+def plan_check(ta, w, pos, seen, lens, n, budget, first, recent, page=64, unaligned=False):
     B, Hkv, cap = w.shape
     pool = torch.zeros(B * n, Hkv, page, 64, dtype=torch.bfloat16, device="cuda")
     cache = ta.AttnCache(pool, pool, i32(lens))
     moves = torch.full((B, Hkv, budget, 2), 9, dtype=torch.int32, device="cuda")
     count = torch.full((B, Hkv), 9, dtype=torch.int32, device="cuda")
-    ta.attn_evict_plan(cache, torch.from_numpy(w).cuda(), i32(pos), i32(seen), moves, count, budget, first, recent)
+    w_t, pos_t = torch.from_numpy(w).cuda(), i32(pos)
+    if unaligned:  # 4 bytes behind a 16-byte boundary
+        off = lambda t: torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)  # noqa: E731
+        w_t, pos_t = off(w_t), off(pos_t)
+    ta.attn_evict_plan(cache, w_t, pos_t, i32(seen), moves, count, budget, first, recent)
     torch.cuda.synchronize()
     want, wn = oracle.cache.evict_plan(w, pos, seen, lens, budget, first, recent)
     assert np.array_equal(count.cpu().numpy(), wn)
@@ -230,6 +234,7 @@ def test_plan(ta, budget, Hkv):
 def test_plan_long(ta, n, budget):
     w, pos, seen, pages = plan_case(n, [n, n - 1], 2, budget, 0)
     plan_check(ta, w, pos, seen, [n, n - 1], pages, budget, 4, budget // 8)
+    plan_check(ta, w, pos, seen, [n, n - 1], pages, budget, 0, 5, unaligned=True)
 
 
 def test_plan_many_heads_and_ranks_that_do_not_fit(ta):

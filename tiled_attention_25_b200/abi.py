@@ -511,6 +511,8 @@ class AttnCache:
         if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("k and v must be [pages][Hkv][page_size][D] pools of one shape")
         self.device = k.device
+        if not k.is_cuda:
+            raise ValueError("k and v must be CUDA tensors")
         P, Hkv, page, D = k.shape
         B = lens.shape[0] if lens.dim() == 1 else 0
         self._own(lens, torch.int32, (B,), "lens")
@@ -523,8 +525,10 @@ class AttnCache:
             self._own(page_table, torch.int32, (B, n), "page_table")
         self.k, self.v, self.lens, self.page_table = k, v, lens, page_table
         self.B, self.Hkv, self.D, self.capacity = B, Hkv, D, n * page
+        self.slots = torch.Size((B, Hkv, n * page))  # of weights and positions
         self.c = CCache(k.data_ptr(), v.data_ptr(), _strides(k, k.shape, "k"), _strides(v, k.shape, "v"),
                         None if page_table is None else page_table.data_ptr(), lens.data_ptr(), B, Hkv, D, P, page, n)
+        self._ref = ctypes.byref(self.c)
         self._own(k, torch.bfloat16, None, "k")
         self._own(v, torch.bfloat16, None, "v")
 
@@ -533,29 +537,44 @@ class AttnCache:
         its pointer (None stays None)."""
         if t is None:
             return None
-        if t.dtype != dtype or t.device != self.device or not t.is_cuda:
+        if t.dtype != dtype or t.device != self.device:
             raise ValueError(f"{what} must be a {dtype} tensor on the cache's CUDA device")
         if shape is not None and (t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor")
         return t.data_ptr()
 
-    def _view(self, t, shape, what):
-        """A bf16 [B][H][S][D] view on the cache's device: its pointer and strides."""
-        if t.device != self.device:
-            raise ValueError(f"{what} must be on the cache's device")
-        return t.data_ptr(), _strides(t, shape, what)
+    def _views(self, **views):
+        """bf16 [B][H][S][D] views (layout member = (tensor or None, shape)):
+        their pointers, and their strides where any is not contiguous."""
+        lay, ptrs = None, []
+        for name, (t, shape) in views.items():
+            if t is None:
+                ptrs.append(None)
+                continue
+            if t.dtype != torch.bfloat16 or t.device != self.device or t.shape != shape:
+                raise ValueError(f"{name} must be a bf16 {tuple(shape)} view on the cache's device")
+            ptrs.append(t.data_ptr())
+            if lay is None and not t.is_contiguous():
+                lay = CLayouts()
+        if lay is not None:
+            for name, (t, shape) in views.items():
+                if t is not None:
+                    setattr(lay, name, _strides(t, shape, name))
+        return ptrs, None if lay is None else ctypes.byref(lay)
 
-    def _call(self, name, stream, *args):
+    def _call(self, name, fn, stream, *args):
         """The C call with the cache's device current, on `stream` (default:
         that device's current stream)."""
+        dev = self.device.index
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        fn = getattr(LIB, name)
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, _stream(stream))
+            raw = torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without a Stream object
         else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, _stream(stream))
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if torch.cuda.current_device() == dev:
+            rc = fn(*args, raw)
+        else:
+            with torch.cuda.device(dev):
+                rc = fn(*args, raw)
         if rc != 0:
             raise AttnError(rc, name)
 
@@ -569,15 +588,12 @@ def attn_cache_append(cache: AttnCache, k_new, v_new, lens_out=None, path=None, 
     """Append (chosen) new K and V rows to the cache (see include/attn25.h).
     k_new, v_new: bf16 [B][Hkv][T][D] views; path: int32 [B][T]; counts,
     seen, lens_out: int32 [B]; positions: int32 [B][Hkv][capacity]."""
-    B, T, own = cache.B, k_new.shape[2], cache._own
+    B, T, own, i32 = cache.B, k_new.shape[2], cache._own, torch.int32
     shape = (B, cache.Hkv, T, cache.D)
-    lay = CLayouts()
-    k_ptr, lay.k = cache._view(k_new, shape, "k_new")
-    v_ptr, lay.v = cache._view(v_new, shape, "v_new")
-    i32 = torch.int32
-    cache._call("attn_cache_append", stream, ctypes.byref(cache.c), k_ptr, v_ptr, own(lens_out, i32, (B,), "lens_out"),
-                own(path, i32, (B, T), "path"), own(counts, i32, (B,), "counts"), T, ctypes.byref(lay),
-                own(positions, i32, (B, cache.Hkv, cache.capacity), "positions"), own(seen, i32, (B,), "seen"))
+    (k_ptr, v_ptr), lay = cache._views(k=(k_new, shape), v=(v_new, shape))
+    cache._call("attn_cache_append", LIB.attn_cache_append, stream, cache._ref, k_ptr, v_ptr,
+                own(lens_out, i32, (B,), "lens_out"), own(path, i32, (B, T), "path"), own(counts, i32, (B,), "counts"), T, lay,
+                own(positions, i32, cache.slots, "positions"), own(seen, i32, (B,), "seen"))
 
 
 def attn_tree_workspace_size(Hq, Hkv, T, D) -> int:
@@ -593,19 +609,12 @@ def attn_tree_fwd(q, k_new, v_new, cache: AttnCache, out, lse, workspace, parent
     _, Hq, T, D = q.shape
     B, own = cache.B, cache._own
     shape, kv_shape = (B, Hq, T, cache.D), (B, cache.Hkv, T, cache.D)
-    lay = CLayouts()
-    q_ptr, lay.q = cache._view(q, shape, "q")
-    o_ptr, lay.out = cache._view(out, shape, "out")
-    k_ptr = v_ptr = None
-    if k_new is not None:
-        k_ptr, lay.k = cache._view(k_new, kv_shape, "k_new")
-    if v_new is not None:
-        v_ptr, lay.v = cache._view(v_new, kv_shape, "v_new")
-    cache._call("attn_tree_fwd", stream, q_ptr, k_ptr, v_ptr, ctypes.byref(cache.c), o_ptr,
+    (q_ptr, k_ptr, v_ptr, o_ptr), lay = cache._views(q=(q, shape), k=(k_new, kv_shape), v=(v_new, kv_shape), out=(out, shape))
+    cache._call("attn_tree_fwd", LIB.attn_tree_fwd, stream, q_ptr, k_ptr, v_ptr, cache._ref, o_ptr,
                 own(lse, torch.float32, (B, Hq, T), "lse"), own(workspace, torch.uint8, None, "workspace"),
                 workspace.numel(), own(parents, torch.int32, (B, T), "parents"),
-                own(counts, torch.int32, (B,), "counts"), Hq, T, D ** -0.5 if scale is None else float(scale),
-                int(mod_kind), _softcap(mod_params), ctypes.byref(lay))
+                own(counts, torch.int32, (B,), "counts"), Hq, T, D ** -0.5 if scale is None else scale,
+                mod_kind, _softcap(mod_params), lay)
 
 
 def attn_cache_weights(q, lse, cache: AttnCache, weights_in, weights_out, path=None, counts=None, scale=None,
@@ -616,13 +625,11 @@ def attn_cache_weights(q, lse, cache: AttnCache, weights_in, weights_out, path=N
     [B][T]; counts: int32 [B]."""
     _, Hq, T, D = q.shape
     B, own, f32 = cache.B, cache._own, torch.float32
-    lay = CLayouts()
-    q_ptr, lay.q = cache._view(q, (B, Hq, T, cache.D), "q")
-    shape = (B, cache.Hkv, cache.capacity)
-    cache._call("attn_cache_weights", stream, q_ptr, own(lse, f32, (B, Hq, T), "lse"), ctypes.byref(cache.c),
-                own(weights_in, f32, shape, "weights_in"), own(weights_out, f32, shape, "weights_out"),
+    (q_ptr,), lay = cache._views(q=(q, (B, Hq, T, cache.D)))
+    cache._call("attn_cache_weights", LIB.attn_cache_weights, stream, q_ptr, own(lse, f32, (B, Hq, T), "lse"), cache._ref,
+                own(weights_in, f32, cache.slots, "weights_in"), own(weights_out, f32, cache.slots, "weights_out"),
                 own(path, torch.int32, (B, T), "path"), own(counts, torch.int32, (B,), "counts"), Hq, T,
-                D ** -0.5 if scale is None else float(scale), int(mod_kind), _softcap(mod_params), ctypes.byref(lay))
+                D ** -0.5 if scale is None else scale, mod_kind, _softcap(mod_params), lay)
 
 
 def attn_evict_plan(cache: AttnCache, weights, positions, seen, moves, n_moves, budget, first=0, recent=0, stream=None):
@@ -630,20 +637,17 @@ def attn_evict_plan(cache: AttnCache, weights, positions, seen, moves, n_moves, 
     positions: int32, both [B][Hkv][capacity]; seen: int32 [B]; moves: int32
     [B][Hkv][budget][2]; n_moves: int32 [B][Hkv]."""
     B, H, own, i32 = cache.B, cache.Hkv, cache._own, torch.int32
-    shape = (B, H, cache.capacity)
-    cache._call("attn_evict_plan", stream, ctypes.byref(cache.c), own(weights, torch.float32, shape, "weights"),
-                own(positions, i32, shape, "positions"), own(seen, i32, (B,), "seen"),
-                own(moves, i32, (B, H, budget, 2), "moves"), own(n_moves, i32, (B, H), "n_moves"), int(budget),
-                int(first), int(recent))
+    cache._call("attn_evict_plan", LIB.attn_evict_plan, stream, cache._ref, own(weights, torch.float32, cache.slots, "weights"),
+                own(positions, i32, cache.slots, "positions"), own(seen, i32, (B,), "seen"),
+                own(moves, i32, (B, H, budget, 2), "moves"), own(n_moves, i32, (B, H), "n_moves"), budget, first, recent)
 
 
 def attn_cache_compact(cache: AttnCache, moves, n_moves, budget, weights=None, positions=None, stream=None):
     """Carry an eviction's moves out (see include/attn25.h)."""
     B, H, own, i32 = cache.B, cache.Hkv, cache._own, torch.int32
-    shape = (B, H, cache.capacity)
-    cache._call("attn_cache_compact", stream, ctypes.byref(cache.c), own(moves, i32, (B, H, budget, 2), "moves"),
-                own(n_moves, i32, (B, H), "n_moves"), int(budget), own(weights, torch.float32, shape, "weights"),
-                own(positions, i32, shape, "positions"))
+    cache._call("attn_cache_compact", LIB.attn_cache_compact, stream, cache._ref, own(moves, i32, (B, H, budget, 2), "moves"),
+                own(n_moves, i32, (B, H), "n_moves"), budget, own(weights, torch.float32, cache.slots, "weights"),
+                own(positions, i32, cache.slots, "positions"))
 
 
 def attn_get_status(stream=None) -> int:

@@ -1,6 +1,7 @@
 // Argument blocks and launchers of the KV-cache kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -13,6 +14,24 @@
 namespace attn25 {
 
 constexpr int kErrIndex = -8;
+
+// Raise a kernel's dynamic shared memory limit, and check the registers it
+// launches with, once per device (`done`: one bit a device, one word a kernel).
+template <class K>
+cudaError_t prepare_kernel(std::atomic<uint64_t>& done, K kernel, int smem, int min_regs) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < min_regs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct CacheDev {
   __nv_bfloat16* k;
@@ -73,7 +92,9 @@ struct PlanArgs {
   int32_t* n_moves;
   int budget, first, recent;
   int* status;
-  int mask_words, held_keys;  // words of a share's masks and ranks of it kept in shared memory (set by the launcher)
+  // set by the launcher: ranks of a CTA's share that fit shared memory; weights and positions on 16 bytes
+  int held_keys;
+  bool aligned;
 };
 
 struct CompactArgs {

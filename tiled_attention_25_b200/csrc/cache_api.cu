@@ -218,7 +218,7 @@ int attn_evict_plan(const attn_cache* cache, const float* weights, const int32_t
   DeviceInfo* d = nullptr;
   rc = current_device(&d);
   if (rc != ATTN_OK) return rc;
-  PlanArgs a{index_of(cache), weights, positions, seen, moves, n_moves, budget, first, recent, d->status, 0, 0};
+  PlanArgs a{index_of(cache), weights, positions, seen, moves, n_moves, budget, first, recent, d->status, 0, false};
   return launched(launch_evict_plan(a, d->sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

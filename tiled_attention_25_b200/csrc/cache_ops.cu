@@ -155,18 +155,23 @@ __device__ __forceinline__ uint32_t slot_rank(float w, int pos, int first, int r
 // One cluster of 1 to 8 CTAs per (row, head), each with an equal share of the
 // slots, whose ranks it keeps in shared memory (read again from global where
 // they do not fit).  A radix select finds the budget-th largest rank in at
-// most three passes of 11, 11 and 10 bits; every CTA adds up the cluster's
-// histograms over distributed shared memory and takes the same decision.  Then
-// each warp walks its part in slot order: ranks of equal ones, kept slots as
-// bit masks, and the places of the holes and of the rows that fill them, from
-// prefix counts over the warps and the CTAs.
-constexpr int kPlanThreads = 512;
+// most three passes of 11, 11 and 10 bits; every CTA adds its filled bins to the
+// histograms of the whole cluster (reductions into distributed shared memory,
+// which nothing waits for until the cluster's barrier; reading the others' bins
+// instead took 10 us a pass) and takes the same decision.  Then
+// each warp walks its part in slot order: ranks of equal ones, kept slots, and
+// the places of the holes and of the rows that fill them, from prefix counts
+// over the lanes, the warps and the CTAs.  A walk's cost is its latency, so a
+// lane takes four neighbouring slots at a time (one 16-byte access): halving 32
+// heads of up to 65000 slots took 34 us with one slot to a lane.
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPlanSmem = 227 * 1024;
 
-struct PlanShared {
-  int hist[3][kBins];
+struct alignas(16) PlanShared {
+  int hist[kBins];      // this CTA's, of the current pass
+  int total[3][kBins];  // the cluster's, of each pass
   int warp_sum[kPlanWarps];
   int tie_warp[kPlanWarps], hole_warp[kPlanWarps], extra_warp[kPlanWarps];
   int ties, holes, extras;  // of this CTA, read by the cluster
@@ -200,6 +205,15 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ void add_cluster(int* p, int v, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .u32 r;\n\t"
+      "mapa.shared::cluster.u32 r, %0, %1;\n\t"
+      "red.relaxed.cluster.shared::cluster.add.s32 [r], %2;\n\t}" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))),
+      "r"(rank), "r"(v)
+      : "memory");
+}
+
 // Sum of the counts of the warps before this one.
 __device__ __forceinline__ int warps_before(const int* counts) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -209,40 +223,46 @@ __device__ __forceinline__ int warps_before(const int* counts) {
   return x;
 }
 
-// Sum of the counts of the CTAs before this one, and of all.
-__device__ __forceinline__ int ctas_before(const int* count, int& all) {
-  int before = 0;
-  all = 0;
-  for (uint32_t c = 0; c < cluster_size(); ++c) {
-    const int v = ld_cluster(count, c);
-    if (c < cluster_rank()) before += v;
-    all += v;
-  }
-  return before;
-}
-
 __device__ __forceinline__ int warp_total(int x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// One more in a bin of the histogram.  Weights of one size share few bins of
-// the first pass, and atomics on one address take turns, so the lanes of a bin
-// are added up first.
-__device__ __forceinline__ void count(int* hist, uint32_t bin, bool in) {
-  const uint32_t active = __activemask();
-  const uint32_t same = __match_any_sync(active, in ? bin : 0xffffffffu);
-  if (in && static_cast<int>(threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+// Sum of the counts of the CTAs before this one, and of all: a lane to a CTA.
+__device__ __forceinline__ int ctas_before(const int* count, int& all) {
+  const uint32_t lane = threadIdx.x & 31;
+  const int v = lane < cluster_size() ? ld_cluster(count, lane) : 0;
+  all = warp_total(v);
+  return warp_total(lane < cluster_rank() ? v : 0);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+// Sum of a count of 0 to 4 over the lanes before this one, and over the warp.
+__device__ __forceinline__ int lanes_before(int x, int& all) {
+  const uint32_t lt = (1u << (threadIdx.x & 31)) - 1u;
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int bit = 0; bit < 3; ++bit) {
+    const uint32_t v = __ballot_sync(0xffffffffu, (x >> bit) & 1);
+    before += __popc(v & lt) << bit;
+    all += __popc(v) << bit;
+  }
+  return before;
+}
+
+// Which of quad q's slots, counted from j0, lie below `end`.
+__device__ __forceinline__ uint32_t quad_below(int end, int j0, int q) {
+  const int left = end - j0 - 4 * q;
+  return left <= 0 ? 0u : (left >= 4 ? 15u : (1u << left) - 1u);
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a) {
   extern __shared__ __align__(16) uint8_t plan_smem[];
   PlanShared& sh = *reinterpret_cast<PlanShared*>(plan_smem);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(plan_smem + sizeof(PlanShared));  // kept slots of the share
-  uint32_t* keys = mask + a.mask_words;
+  uint4* keys = reinterpret_cast<uint4*>(plan_smem + sizeof(PlanShared));  // ranks of the share
+  uint8_t* kept = plan_smem + sizeof(PlanShared) + a.held_keys * 4;        // its kept slots, four to a byte
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t lt = (1u << lane) - 1u;
   const int ctas = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int bh = blockIdx.x / ctas, b = bh / a.ix.Hkv;
   bool bad = false;
@@ -254,48 +274,78 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const float* w = a.weights + static_cast<long long>(bh) * a.ix.capacity;
     const int32_t* pos = a.positions + static_cast<long long>(bh) * a.ix.capacity;
     const int recent_from = a.seen[b] - a.recent;
-    // this CTA's slots [j0, j0 + m), whole words of the masks
+    // this CTA's slots [j0, j0 + m) in quads of four
     const int share = ((n + ctas - 1) / ctas + 31) / 32 * 32;
-    const int j0 = min(n, rank * share), m = min(n - j0, share);
+    const int j0 = min(n, rank * share), m = min(n - j0, share), quads = (m + 3) / 4;
     const bool held = share <= a.held_keys;
-    auto fresh = [&](int i) { return slot_rank(w[j0 + i], pos[j0 + i], a.first, recent_from); };
-    auto key = [&](int i) { return held ? keys[i] : fresh(i); };
-    for (int i = threadIdx.x; i < 3 * kBins; i += kPlanThreads) (&sh.hist[0][0])[i] = 0;
-    __syncthreads();
+    auto fresh = [&](int q) {
+      uint32_t k[4] = {0u, 0u, 0u, 0u};
+      const int j = j0 + 4 * q;
+      if (a.aligned && 4 * q + 4 <= m) {
+        const float4 x = *reinterpret_cast<const float4*>(w + j);
+        const int4 y = *reinterpret_cast<const int4*>(pos + j);
+        k[0] = slot_rank(x.x, y.x, a.first, recent_from);
+        k[1] = slot_rank(x.y, y.y, a.first, recent_from);
+        k[2] = slot_rank(x.z, y.z, a.first, recent_from);
+        k[3] = slot_rank(x.w, y.w, a.first, recent_from);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * q + e < m) k[e] = slot_rank(w[j + e], pos[j + e], a.first, recent_from);
+      }
+      return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+    auto quad = [&](int q) { return held ? keys[q] : fresh(q); };
+    // f(rank, bit of the quad) for the slots of quad q that exist
+    auto each = [&](int q, const uint4& k, auto f) {
+      const int left = m - 4 * q;
+      if (left > 0) f(k.x, 1u);
+      if (left > 1) f(k.y, 2u);
+      if (left > 2) f(k.z, 4u);
+      if (left > 3) f(k.w, 8u);
+    };
+    for (int i = threadIdx.x; i < 3 * kBins; i += kPlanThreads) (&sh.total[0][0])[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kPlanThreads) sh.hist[i] = 0;
+    if (ctas > 1) cluster_sync();  // the others add to the totals
+    else __syncthreads();
     uint32_t prefix = 0;     // the bits decided so far
     int need = a.budget;     // slots still to take among those that share them
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bins = pass == 2 ? 1024 : kBins;
       const int above = pass == 0 ? 32 : (pass == 1 ? 21 : 10);  // bits below the decided ones
-      int* hist = sh.hist[pass];
       if (pass == 0) {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < m; i += kPlanThreads) {
-          const uint32_t k = fresh(i);
-          if (held) keys[i] = k;
-          count(hist, k >> shift, true);
+        for (int q = threadIdx.x; q < quads; q += kPlanThreads) {
+          const uint4 k = fresh(q);
+          if (held) keys[q] = k;
+          each(q, k, [&](uint32_t x, uint32_t) { atomicAdd(&sh.hist[x >> shift], 1); });
         }
       } else {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < m; i += kPlanThreads) {
-          const uint32_t k = key(i);
-          count(hist, (k >> shift) & (bins - 1), (k >> above) == (prefix >> above));
-        }
+        for (int q = threadIdx.x; q < quads; q += kPlanThreads)
+          each(q, quad(q), [&](uint32_t x, uint32_t) {
+            if ((x >> above) == (prefix >> above)) atomicAdd(&sh.hist[(x >> shift) & (bins - 1)], 1);
+          });
       }
-      if (ctas > 1) cluster_sync();
-      else __syncthreads();
-      // the bin in which the count from the top reaches `need`: four bins to a thread, from the top
-      int c[4], sum = 0;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int bin = bins - 1 - (4 * static_cast<int>(threadIdx.x) + x);
-        c[x] = 0;
-        if (bin >= 0) {
-          if (ctas == 1) c[x] = hist[bin];
-          else
-            for (int q = 0; q < ctas; ++q) c[x] += ld_cluster(&hist[bin], q);
+      __syncthreads();
+      int* total = sh.hist;
+      if (ctas > 1) {
+        total = sh.total[pass];
+        for (int i = threadIdx.x; i < bins; i += kPlanThreads) {
+          const int v = sh.hist[i];
+          if (v != 0) {
+            sh.hist[i] = 0;
+            for (int q = 0; q < ctas; ++q) add_cluster(&total[i], v, q);
+          }
         }
+        cluster_sync();
+      }
+      // the bin in which the count from the top reaches `need`: two bins to a thread, from the top
+      int c[2], sum = 0;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int bin = bins - 1 - (2 * static_cast<int>(threadIdx.x) + x);
+        c[x] = bin >= 0 ? total[bin] : 0;
+        if (ctas == 1 && bin >= 0) total[bin] = 0;  // for the next pass
         sum += c[x];
       }
       int inc = sum;
@@ -308,11 +358,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       __syncthreads();
       int before = warps_before(sh.warp_sum) + inc - sum;
       if (before < need && before + sum >= need) {
-        int x = 0;
-        while (before + c[x] < need) before += c[x++];
-        sh.digit = bins - 1 - (4 * threadIdx.x + x);
+        const int x = before + c[0] < need ? 1 : 0;
+        if (x == 1) before += c[0];
+        sh.digit = bins - 1 - (2 * threadIdx.x + x);
         sh.need = need - before;
-        sh.in_bin = c[x];
+        sh.in_bin = x == 1 ? c[1] : c[0];
       }
       __syncthreads();
       prefix |= sh.digit << shift;
@@ -324,45 +374,56 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       }
     }
     // slots of rank above `prefix` stay, and the first `need` (in slot order) of equal rank
-    const int words = (m + 31) / 32, per = (words + kPlanWarps - 1) / kPlanWarps;
-    const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
+    const int per = (quads + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * 32;  // quads of a warp
+    const int q0 = min(quads, warp * per), q1 = min(quads, q0 + per);
     int t = 0;
     if (need > 0)
-      for (int x = w0; x < w1; ++x) {
-        const int i = x * 32 + lane;
-        t += i < m && key(i) == prefix;
-      }
+      for (int q = q0 + lane; q < q1; q += 32) each(q, quad(q), [&](uint32_t k, uint32_t) { t += k == prefix; });
     t = warp_total(t);
     if (lane == 0) sh.tie_warp[warp] = t;
     __syncthreads();
     if (warp == 0) {
-      const int v = warp_total(lane < kPlanWarps ? sh.tie_warp[lane] : 0);
+      const int v = warp_total(sh.tie_warp[lane]);
       if (lane == 0) sh.ties = v;
     }
     if (ctas > 1) cluster_sync();
     else __syncthreads();
     int all;
     int tie = ctas_before(&sh.ties, all) + warps_before(sh.tie_warp);
-    int holes = 0, extras = 0;
-    for (int x = w0; x < w1; ++x) {
-      const int i = x * 32 + lane;
-      const uint32_t k = i < m ? key(i) : 0u;
-      const uint32_t eq = __ballot_sync(0xffffffffu, need > 0 && i < m && k == prefix);
-      const bool keep = i < m && (k > prefix || (((eq >> lane) & 1u) && tie + __popc(eq & lt) < need));
-      tie += __popc(eq);
-      const uint32_t kept = __ballot_sync(0xffffffffu, keep), low = __ballot_sync(0xffffffffu, i < m && j0 + i < a.budget);
-      if (lane == 0) mask[x] = kept;
-      holes += __popc(low & ~kept);
-      extras += __popc(kept & ~low);
+    int holes = 0, extras = 0;  // of this lane
+    for (int qb = q0; qb < q1; qb += 32) {
+      const int q = qb + lane;
+      uint32_t keep = 0, eq = 0;
+      if (q < q1)
+        each(q, quad(q), [&](uint32_t k, uint32_t bit) {
+          if (k > prefix) keep |= bit;
+          if (need > 0 && k == prefix) eq |= bit;
+        });
+      if (need > 0) {  // the first of equal rank, in slot order
+        int here = 0, rank_of = tie + lanes_before(__popc(eq), here);
+        tie += here;
+#pragma unroll
+        for (uint32_t bit = 1; bit < 16; bit <<= 1)
+          if (eq & bit) {
+            if (rank_of < need) keep |= bit;
+            ++rank_of;
+          }
+      }
+      if (q < q1) {
+        kept[q] = static_cast<uint8_t>(keep);
+        const uint32_t low = quad_below(a.budget, j0, q), there = quad_below(m, 0, q);
+        holes += __popc(low & there & ~keep);
+        extras += __popc(keep & ~low);
+      }
     }
+    const int warp_holes = warp_total(holes), warp_extras = warp_total(extras);
     if (lane == 0) {
-      sh.hole_warp[warp] = holes;
-      sh.extra_warp[warp] = extras;
+      sh.hole_warp[warp] = warp_holes;
+      sh.extra_warp[warp] = warp_extras;
     }
     __syncthreads();
     if (warp == 0) {
-      const int h = warp_total(lane < kPlanWarps ? sh.hole_warp[lane] : 0);
-      const int e = warp_total(lane < kPlanWarps ? sh.extra_warp[lane] : 0);
+      const int h = warp_total(sh.hole_warp[lane]), e = warp_total(sh.extra_warp[lane]);
       if (lane == 0) {
         sh.holes = h;
         sh.extras = e;
@@ -372,14 +433,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     else __syncthreads();
     int at_h = ctas_before(&sh.holes, n_moves) + warps_before(sh.hole_warp);
     int at_e = ctas_before(&sh.extras, all) + warps_before(sh.extra_warp);
-    for (int x = w0; x < w1; ++x) {
-      const int j = j0 + x * 32 + lane;
-      const uint32_t kept = mask[x], low = __ballot_sync(0xffffffffu, j < a.budget && j < n);
-      const uint32_t hole = low & ~kept, extra = kept & ~low;
-      if ((hole >> lane) & 1u) moves[at_h + __popc(hole & lt)].x = j;
-      if ((extra >> lane) & 1u) moves[at_e + __popc(extra & lt)].y = j;
-      at_h += __popc(hole);
-      at_e += __popc(extra);
+    for (int qb = q0; qb < q1; qb += 32) {
+      const int q = qb + lane, j = j0 + 4 * q;
+      uint32_t hole = 0, extra = 0;
+      if (q < q1) {
+        const uint32_t keep = kept[q], low = quad_below(a.budget, j0, q);
+        hole = low & quad_below(m, 0, q) & ~keep;
+        extra = keep & ~low;
+      }
+      int here_h = 0, here_e = 0;
+      int to = at_h + lanes_before(__popc(hole), here_h), from = at_e + lanes_before(__popc(extra), here_e);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((hole >> e) & 1u) moves[to++].x = j + e;
+        if ((extra >> e) & 1u) moves[from++].y = j + e;
+      }
+      at_h += here_h;
+      at_e += here_e;
     }
     if (ctas > 1) cluster_sync();  // the others may still read this CTA's counts
   }
@@ -417,15 +487,16 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
 cudaError_t launch_evict_plan(const PlanArgs& args, int sms, cudaStream_t stream) {
   PlanArgs a = args;
   const int heads = a.ix.B * a.ix.Hkv;
-  // CTAs to a head: more while they do not fill the SMs twice over and every one keeps 2048 slots
+  // CTAs to a head: more while one to an SM is not exceeded and each keeps a quad for every thread
   int ctas = 1;
-  while (ctas < 8 && heads * ctas * 2 <= 2 * sms && a.ix.capacity / (ctas * 2) >= 2048) ctas *= 2;
+  while (ctas < 8 && heads * ctas * 2 <= sms && a.ix.capacity / (ctas * 2) >= 4 * kPlanThreads) ctas *= 2;
   const int share = ((a.ix.capacity + ctas - 1) / ctas + 31) / 32 * 32;
-  a.mask_words = share / 32;
-  const int room = (kPlanSmem - static_cast<int>(sizeof(PlanShared))) / 4 - a.mask_words;
+  const int room = (kPlanSmem - static_cast<int>(sizeof(PlanShared)) - share / 4) / 16 * 4;
   a.held_keys = share < room ? share : room;  // a row shorter than the capacity has a smaller share
-  const size_t smem = sizeof(PlanShared) + (static_cast<size_t>(a.mask_words) + a.held_keys) * 4;
-  cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  a.aligned = ((reinterpret_cast<uintptr_t>(a.weights) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  const size_t smem = sizeof(PlanShared) + static_cast<size_t>(a.held_keys) * 4 + share / 4;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = prepare_kernel(done, plan_kernel, kPlanSmem, 0);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(heads * ctas);

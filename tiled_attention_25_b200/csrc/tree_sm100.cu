@@ -744,11 +744,8 @@ template <int D, bool SOFTCAP>
 cudaError_t launch_tree_t(const TreeMaps& m, const TreeParams& p, cudaStream_t stream) {
   auto kernel = attn_tree_kernel<D, SOFTCAP>;
   // the register split assumes kTreeLaunchRegs at launch; with fewer, setmaxnreg.inc could wait forever
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < kTreeLaunchRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeCfg<D>::kAllocBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = prepare_kernel(done, kernel, TreeCfg<D>::kAllocBytes, kTreeLaunchRegs);
   if (e != cudaSuccess) return e;
   kernel<<<p.groups * p.rt.tiles, kTreeThreads, TreeCfg<D>::kAllocBytes, stream>>>(m.q, m.k, m.v, m.kn, m.vn, p);
   e = cudaGetLastError();

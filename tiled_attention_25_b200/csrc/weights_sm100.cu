@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
 template <int D, bool SOFTCAP>
 cudaError_t launch_weights_t(const CUtensorMap& tq, const CUtensorMap& tk, const WParams& p, int sms, cudaStream_t stream) {
   auto kernel = cache_weights_kernel<D, SOFTCAP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg<D>::kAllocBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = prepare_kernel(done, kernel, WCfg<D>::kAllocBytes, 0);
   if (e != cudaSuccess) return e;
   kernel<<<sms, kWThreads, WCfg<D>::kAllocBytes, stream>>>(tq, tk, p);
   return cudaGetLastError();
