@@ -4,8 +4,8 @@ interleavings of its warp roles (CPU only).
 Roles as in ``tiled_attention_25_b200/csrc/tree_sm100.cu``, with its barrier
 counts and phases (a group of warps that arrive together is one arrival):
 
-* the TMA warp publishes pieces (a number of 128-key steps), loads Q and
-  streams K and V through the ring in the order K0 K1 V0 K2 V1 ... V(n-1);
+* one TMA warp publishes pieces (a number of 128-key steps), loads Q (into one
+  buffer, or two in turn) and streams K through its ring, a second streams V;
 * the MMA warp issues S(j) and O(j) alternately for the two softmax
   warpgroups, which take the even and the odd steps;
 * on a step with missing keys a softmax warpgroup first waits for that step's
@@ -20,87 +20,105 @@ import pytest
 from protocol_sim import Sim
 
 
-def roles(sim, pieces, partial, stages):
+def roles(sim, pieces, partial, stages, q_bufs=2):
     """pieces: steps of each; partial: the (piece, step) whose V is zeroed in part."""
     full, empty, drain = sim.full, sim.empty, sim.drain
     for b in range(2):
         sim.bar(f"list_full{b}", 1)
-        sim.bar(f"list_empty{b}", 3)
+        sim.bar(f"list_empty{b}", 4)
         sim.bar(f"s_full{b}", 1)
         sim.bar(f"p_full{b}", 1)
         sim.bar(f"o_full{b}", 1)
-    for name, count in (("q_full", 1), ("q_empty", 1), ("o_final", 1), ("epi_done", 2), ("ml_ready", 2), ("drain", 1)):
+        sim.bar(f"q_full{b}", 1)
+        sim.bar(f"q_empty{b}", 1)
+    for name, count in (("o_final", 1), ("s_free", 2), ("epi_done", 2), ("ml_ready", 2), ("drain", 1)):
         sim.bar(name, count)
     for s in range(stages):
-        sim.bar(f"kv_full{s}", 1)
-        sim.bar(f"kv_empty{s}", 1)
+        for kv in "kv":
+            sim.bar(f"{kv}_full{s}", 1)
+            sim.bar(f"{kv}_empty{s}", 1)
     walk = list(pieces) + [None]
 
-    def v_at(j, n):
-        return 2 * j + 2 if j < n - 1 else 2 * n - 1
+    def copies(kv, n, done):
+        for _ in range(n):
+            if not (yield empty(f"{kv}_empty{done[0] % stages}", done[0] // stages)):
+                return False
+            sim.load(f"{kv}_full{done[0] % stages}")
+            done[0] += 1
+        return True
+
+    def drain_ring(kv, done):
+        for s in range(stages):
+            if (uses := (done[0] + stages - 1 - s) // stages):
+                yield drain(f"{kv}_full{s}", uses - 1)
 
     def tma():
-        ring = q_loads = 0
+        done, q_loads = [0], 0
 
         def body():
-            nonlocal ring, q_loads
+            nonlocal q_loads
             for u, n in enumerate(walk):
                 if not (yield empty(f"list_empty{u & 1}", u >> 1)):
                     return
                 sim.arrive(f"list_full{u & 1}")
                 if n is None:
                     return
-                if not (yield empty("q_empty", u)):
+                if not (yield empty(f"q_empty{u % q_bufs}", u // q_bufs)):
                     return
-                sim.load("q_full")
+                sim.load(f"q_full{u % q_bufs}")
                 q_loads += 1
-                for _ in range(2 * n):
-                    slot = ring % stages
-                    if not (yield empty(f"kv_empty{slot}", ring // stages)):
-                        return
-                    sim.load(f"kv_full{slot}")
-                    ring += 1
+                if not (yield from copies("k", n, done)):
+                    return
         yield from body()
-        for s in range(stages):
-            uses = (ring + stages - 1 - s) // stages
-            if uses:
-                yield drain(f"kv_full{s}", uses - 1)
-        if q_loads:
-            yield drain("q_full", q_loads - 1)
+        yield from drain_ring("k", done)
+        for s in range(q_bufs):
+            if (uses := (q_loads + q_bufs - 1 - s) // q_bufs):
+                yield drain(f"q_full{s}", uses - 1)
+
+    def tma_v():
+        done = [0]
+        for u, n in enumerate(walk):
+            if not (yield full(f"list_full{u & 1}", u >> 1)):
+                break
+            sim.arrive(f"list_empty{u & 1}")
+            if n is None or not (yield from copies("v", n, done)):
+                break
+        yield from drain_ring("v", done)
 
     def mma():
-        ring, p_cnt = 0, [0, 0]
+        kn, vn, p_cnt = 0, 0, [0, 0]
 
         def qk(t):
-            nonlocal ring
-            slot = ring % stages
-            if not (yield full(f"kv_full{slot}", ring // stages)):
+            nonlocal kn
+            if not (yield full(f"k_full{kn % stages}", kn // stages)):
                 return False
             sim.commit(f"s_full{t}")
-            sim.commit(f"kv_empty{slot}")
-            ring += 1
+            sim.commit(f"k_empty{kn % stages}")
+            kn += 1
             return True
 
         def body():
-            nonlocal ring
+            nonlocal vn
             for u, n in enumerate(walk):
                 if not (yield full(f"list_full{u & 1}", u >> 1)) or n is None:
                     return
-                if not (yield empty("epi_done", u)) or not (yield full("q_full", u)):
+                if not (yield empty("s_free", u)) or not (yield full(f"q_full{u % q_bufs}", u // q_bufs)):
                     return
                 if not (yield from qk(0)) or (n > 1 and not (yield from qk(1))):
                     return
+                if not (yield empty("epi_done", u)):
+                    return
                 for j in range(n):
-                    t, slot = j & 1, ring % stages
-                    if not (yield full(f"kv_full{slot}", ring // stages)) or not (yield full(f"p_full{t}", p_cnt[t])):
+                    t = j & 1
+                    if not (yield full(f"v_full{vn % stages}", vn // stages)) or not (yield full(f"p_full{t}", p_cnt[t])):
                         return
                     p_cnt[t] += 1
                     sim.commit(f"o_full{t}")
-                    sim.commit(f"kv_empty{slot}")
-                    ring += 1
+                    sim.commit(f"v_empty{vn % stages}")
+                    vn += 1
                     if j + 2 < n and not (yield from qk(t)):
                         return
-                sim.commit("q_empty")
+                sim.commit(f"q_empty{u % q_bufs}")
                 sim.commit("o_final")
                 sim.arrive(f"list_empty{u & 1}")
         yield from body()
@@ -120,43 +138,44 @@ def roles(sim, pieces, partial, stages):
                     if not (yield full(f"o_full{t}", s_cnt - 2)):
                         return
                 if (u, j) in partial:
-                    pos = base + v_at(j, n)
-                    if not (yield full(f"kv_full{pos % stages}", pos // stages)):
+                    if not (yield full(f"v_full{(base + j) % stages}", (base + j) // stages)):
                         return
                 sim.arrive(f"p_full{t}")
-            base += 2 * n
+            base += n
             if not (yield full("o_final", u)):
                 return
             sim.arrive("ml_ready")
             if not (yield full("ml_ready", u)):
                 return
+            sim.arrive("s_free")
             sim.arrive("epi_done")
             sim.arrive(f"list_empty{u & 1}")
 
-    return {"tma": tma(), "mma": mma(), "softmax0": softmax(0), "softmax1": softmax(1)}
+    return {"tma": tma(), "tma_v": tma_v(), "mma": mma(), "softmax0": softmax(0), "softmax1": softmax(1)}
 
 
 PIECES = {"one": [1], "two": [2], "long": [17], "short": [1, 1, 1, 1, 1], "mixed": [3, 1, 2, 8, 1, 5], "none": []}
 
 
-@pytest.mark.parametrize("stages", [6, 12])
+@pytest.mark.parametrize("q_bufs", [1, 2])
+@pytest.mark.parametrize("stages", [3, 6])
 @pytest.mark.parametrize("name", sorted(PIECES))
-def test_tree_protocol_never_deadlocks_or_aliases(name, stages):
+def test_tree_protocol_never_deadlocks_or_aliases(name, stages, q_bufs):
     pieces = PIECES[name]
     for seed in range(150):
         sim = Sim(seed)
         partial = {(u, n - 1) for u, n in enumerate(pieces)} | {(u, n - 2) for u, n in enumerate(pieces) if seed & 1}
-        stuck = sim.run(roles(sim, pieces, partial, stages))
+        stuck = sim.run(roles(sim, pieces, partial, stages, q_bufs))
         assert stuck is None, f"{name}, seed {seed}: {stuck}"
         assert sim.in_flight_at_exit == 0
 
 
-@pytest.mark.parametrize("role", ["tma", "mma", "softmax0", "softmax1"])
+@pytest.mark.parametrize("role", ["tma", "tma_v", "mma", "softmax0", "softmax1"])
 def test_a_wait_that_runs_out_ends_every_role(role):
     for at in range(25):
         for seed in range(12):
             sim = Sim(seed)
-            stuck = sim.run(roles(sim, PIECES["mixed"], {(0, 2), (3, 7)}, 6), give_up=(role, at))
+            stuck = sim.run(roles(sim, PIECES["mixed"], {(0, 2), (3, 7)}, 3), give_up=(role, at))
             assert stuck is None, f"{role} wait {at}, seed {seed}: {stuck}"
             assert sim.in_flight_at_exit == 0, f"{role} wait {at}, seed {seed}: {sim.pending_at_exit}"
 
