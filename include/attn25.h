@@ -425,10 +425,13 @@ ATTN25_API int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new
  * mod_kind: ATTN_MOD_NONE or ATTN_MOD_SOFTCAP (slots of a cache that has
  * evicted some have no index to mask by; ATTN_ERR_UNSUPPORTED otherwise).
  * workspace: device memory of at least attn_tree_workspace_size bytes,
- * 256-byte aligned; its contents on entry do not matter, and calls that
- * overlap in time need one each.  The result is the same bit for bit on
- * every run.
+ * 256-byte aligned, whose first ATTN_TREE_COUNTER_BYTES are zero: zero them
+ * once before the first use (and after a call that reported
+ * ATTN_ERR_TIMEOUT); every call leaves them zero again.  The rest may hold
+ * anything.  Calls that overlap in time need a workspace each.  The result
+ * is the same bit for bit on every run.
  */
+#define ATTN_TREE_COUNTER_BYTES 1024
 ATTN25_API size_t attn_tree_workspace_size(int Hq, int Hkv, int T, int D);
 ATTN25_API int attn_tree_fwd(const attn_bf16* q, const attn_bf16* k_new, const attn_bf16* v_new,
                              const attn_cache* cache, attn_bf16* out, float* lse, void* workspace,

@@ -4,13 +4,13 @@ interleavings of its warp roles (CPU only).
 Roles as in ``tiled_attention_25_b200/csrc/tree_sm100.cu``, with its barrier
 counts and phases (a group of warps that arrive together is one arrival):
 
-* one TMA warp publishes pieces (a number of 128-key steps), loads Q (into one
-  buffer, or two in turn) and streams K through its ring, a second streams V;
+* one TMA warp publishes pieces (a number of 128-key steps) and streams K
+  through its ring, a second streams V, a third loads each piece's Q;
 * the MMA warp issues S(j) and O(j) alternately for the two softmax
   warpgroups, which take the even and the odd steps;
 * on a step with missing keys a softmax warpgroup first waits for that step's
   V itself (it zeroes rows of it); at the end of a piece the two exchange
-  their running values and the next piece's products wait for both.
+  their running values and join O, which the next piece's first O waits for.
 
 Checks: no deadlock, no aliasing, and with any one wait of any role running
 out, every role ends with no copy or product in flight.
@@ -20,60 +20,62 @@ import pytest
 from protocol_sim import Sim
 
 
-def roles(sim, pieces, partial, stages, q_bufs=2):
-    """pieces: steps of each; partial: the (piece, step) whose V is zeroed in part."""
+def roles(sim, pieces, partial, stages):
+    """pieces: steps of each; stages: of the K and the V ring; partial: the (piece, step) whose V is zeroed in part."""
     full, empty, drain = sim.full, sim.empty, sim.drain
     for b in range(2):
         sim.bar(f"list_full{b}", 1)
-        sim.bar(f"list_empty{b}", 4)
+        sim.bar(f"list_empty{b}", 5)
         sim.bar(f"s_full{b}", 1)
         sim.bar(f"p_full{b}", 1)
         sim.bar(f"o_full{b}", 1)
-        sim.bar(f"q_full{b}", 1)
-        sim.bar(f"q_empty{b}", 1)
-    for name, count in (("o_final", 1), ("s_free", 2), ("epi_done", 2), ("ml_ready", 2), ("drain", 1)):
+    for name, count in (("q_full", 1), ("q_empty", 1), ("o_final", 1), ("epi_done", 2), ("ml_ready", 2), ("drain", 1)):
         sim.bar(name, count)
-    for s in range(stages):
-        for kv in "kv":
+    stages = dict(zip("kv", stages))
+    for kv in "kv":
+        for s in range(stages[kv]):
             sim.bar(f"{kv}_full{s}", 1)
             sim.bar(f"{kv}_empty{s}", 1)
     walk = list(pieces) + [None]
 
     def copies(kv, n, done):
         for _ in range(n):
-            if not (yield empty(f"{kv}_empty{done[0] % stages}", done[0] // stages)):
+            if not (yield empty(f"{kv}_empty{done[0] % stages[kv]}", done[0] // stages[kv])):
                 return False
-            sim.load(f"{kv}_full{done[0] % stages}")
+            sim.load(f"{kv}_full{done[0] % stages[kv]}")
             done[0] += 1
         return True
 
     def drain_ring(kv, done):
-        for s in range(stages):
-            if (uses := (done[0] + stages - 1 - s) // stages):
+        for s in range(stages[kv]):
+            if (uses := (done[0] + stages[kv] - 1 - s) // stages[kv]):
                 yield drain(f"{kv}_full{s}", uses - 1)
 
     def tma():
-        done, q_loads = [0], 0
+        done = [0]
 
         def body():
-            nonlocal q_loads
             for u, n in enumerate(walk):
                 if not (yield empty(f"list_empty{u & 1}", u >> 1)):
                     return
                 sim.arrive(f"list_full{u & 1}")
-                if n is None:
-                    return
-                if not (yield empty(f"q_empty{u % q_bufs}", u // q_bufs)):
-                    return
-                sim.load(f"q_full{u % q_bufs}")
-                q_loads += 1
-                if not (yield from copies("k", n, done)):
+                if n is None or not (yield from copies("k", n, done)):
                     return
         yield from body()
         yield from drain_ring("k", done)
-        for s in range(q_bufs):
-            if (uses := (q_loads + q_bufs - 1 - s) // q_bufs):
-                yield drain(f"q_full{s}", uses - 1)
+
+    def tma_q():
+        loads = 0
+        for u, n in enumerate(walk):
+            if not (yield full(f"list_full{u & 1}", u >> 1)):
+                break
+            sim.arrive(f"list_empty{u & 1}")
+            if n is None or not (yield empty("q_empty", u)):
+                break
+            sim.load("q_full")
+            loads += 1
+        if loads:
+            yield drain("q_full", loads - 1)
 
     def tma_v():
         done = [0]
@@ -88,37 +90,34 @@ def roles(sim, pieces, partial, stages, q_bufs=2):
     def mma():
         kn, vn, p_cnt = 0, 0, [0, 0]
 
-        def qk(t):
-            nonlocal kn
-            if not (yield full(f"k_full{kn % stages}", kn // stages)):
-                return False
-            sim.commit(f"s_full{t}")
-            sim.commit(f"k_empty{kn % stages}")
-            kn += 1
-            return True
-
         def body():
-            nonlocal vn
+            nonlocal kn, vn
             for u, n in enumerate(walk):
                 if not (yield full(f"list_full{u & 1}", u >> 1)) or n is None:
                     return
-                if not (yield empty("s_free", u)) or not (yield full(f"q_full{u % q_bufs}", u // q_bufs)):
+                if not (yield full("q_full", u)):
                     return
-                if not (yield from qk(0)) or (n > 1 and not (yield from qk(1))):
-                    return
-                if not (yield empty("epi_done", u)):
-                    return
-                for j in range(n):
-                    t = j & 1
-                    if not (yield full(f"v_full{vn % stages}", vn // stages)) or not (yield full(f"p_full{t}", p_cnt[t])):
-                        return
-                    p_cnt[t] += 1
-                    sim.commit(f"o_full{t}")
-                    sim.commit(f"v_empty{vn % stages}")
-                    vn += 1
-                    if j + 2 < n and not (yield from qk(t)):
-                        return
-                sim.commit(f"q_empty{u % q_bufs}")
+                for i in range(n + 2):
+                    t = i & 1
+                    if i >= 2 and i - 2 < n:
+                        if i == 2 and not (yield empty("epi_done", u)):
+                            return
+                        if not (yield full(f"v_full{vn % stages['v']}", vn // stages["v"])):
+                            return
+                        if not (yield full(f"p_full{t}", p_cnt[t])):
+                            return
+                        p_cnt[t] += 1
+                        sim.commit(f"o_full{t}")
+                        sim.commit(f"v_empty{vn % stages['v']}")
+                        vn += 1
+                    if i < n:
+                        if not (yield full(f"k_full{kn % stages['k']}", kn // stages["k"])):
+                            return
+                        sim.commit(f"s_full{t}")
+                        sim.commit(f"k_empty{kn % stages['k']}")
+                        if i == n - 1:
+                            sim.commit("q_empty")
+                        kn += 1
                 sim.commit("o_final")
                 sim.arrive(f"list_empty{u & 1}")
         yield from body()
@@ -138,7 +137,7 @@ def roles(sim, pieces, partial, stages, q_bufs=2):
                     if not (yield full(f"o_full{t}", s_cnt - 2)):
                         return
                 if (u, j) in partial:
-                    if not (yield full(f"v_full{(base + j) % stages}", (base + j) // stages)):
+                    if not (yield full(f"v_full{(base + j) % stages['v']}", (base + j) // stages["v"])):
                         return
                 sim.arrive(f"p_full{t}")
             base += n
@@ -147,35 +146,33 @@ def roles(sim, pieces, partial, stages, q_bufs=2):
             sim.arrive("ml_ready")
             if not (yield full("ml_ready", u)):
                 return
-            sim.arrive("s_free")
             sim.arrive("epi_done")
             sim.arrive(f"list_empty{u & 1}")
 
-    return {"tma": tma(), "tma_v": tma_v(), "mma": mma(), "softmax0": softmax(0), "softmax1": softmax(1)}
+    return {"tma": tma(), "tma_v": tma_v(), "tma_q": tma_q(), "mma": mma(), "softmax0": softmax(0), "softmax1": softmax(1)}
 
 
 PIECES = {"one": [1], "two": [2], "long": [17], "short": [1, 1, 1, 1, 1], "mixed": [3, 1, 2, 8, 1, 5], "none": []}
 
 
-@pytest.mark.parametrize("q_bufs", [1, 2])
-@pytest.mark.parametrize("stages", [3, 6])
+@pytest.mark.parametrize("stages", [(3, 2), (6, 5)])
 @pytest.mark.parametrize("name", sorted(PIECES))
-def test_tree_protocol_never_deadlocks_or_aliases(name, stages, q_bufs):
+def test_tree_protocol_never_deadlocks_or_aliases(name, stages):
     pieces = PIECES[name]
     for seed in range(150):
         sim = Sim(seed)
         partial = {(u, n - 1) for u, n in enumerate(pieces)} | {(u, n - 2) for u, n in enumerate(pieces) if seed & 1}
-        stuck = sim.run(roles(sim, pieces, partial, stages, q_bufs))
+        stuck = sim.run(roles(sim, pieces, partial, stages))
         assert stuck is None, f"{name}, seed {seed}: {stuck}"
         assert sim.in_flight_at_exit == 0
 
 
-@pytest.mark.parametrize("role", ["tma", "tma_v", "mma", "softmax0", "softmax1"])
+@pytest.mark.parametrize("role", ["tma", "tma_v", "tma_q", "mma", "softmax0", "softmax1"])
 def test_a_wait_that_runs_out_ends_every_role(role):
     for at in range(25):
         for seed in range(12):
             sim = Sim(seed)
-            stuck = sim.run(roles(sim, PIECES["mixed"], {(0, 2), (3, 7)}, 3), give_up=(role, at))
+            stuck = sim.run(roles(sim, PIECES["mixed"], {(0, 2), (3, 7)}, (3, 2)), give_up=(role, at))
             assert stuck is None, f"{role} wait {at}, seed {seed}: {stuck}"
             assert sim.in_flight_at_exit == 0, f"{role} wait {at}, seed {seed}: {sim.pending_at_exit}"
 

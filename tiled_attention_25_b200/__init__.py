@@ -92,9 +92,9 @@ def new_attn_cache(B, Hkv, capacity, D, page_size=64, device="cuda") -> AttnCach
 
 
 def new_tree_workspace(Hq, Hkv, T, D, device="cuda") -> torch.Tensor:
-    """A 256-byte-aligned workspace of attn_tree_workspace_size bytes (good
-    for every call of up to T tokens with these heads)."""
+    """A 256-byte-aligned, zeroed workspace of attn_tree_workspace_size bytes
+    (good for every call of up to T tokens with these heads)."""
     nbytes = attn_tree_workspace_size(Hq, Hkv, T, D)
-    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % 256
     return buf[off:off + nbytes]

@@ -73,13 +73,19 @@ ATTN25_HD RowTiles row_tiles(int G, int T) {
 
 // ------------------------------------------------------------------ work split
 //
-// The steps (128 keys each) of all items (row b, KV head) in order form one
-// stream, cut into `groups` equal ranges; the `tiles` CTAs of a group take one
-// query tile each over the same range, so that they share its K and V in L2.
-// A range's part of an item is a piece; an item cut over several groups leaves
-// partial results that are joined afterwards.  The cut depends on the lengths
-// alone, so results are the same on every run.
+// An item is one row's work for one KV head: its steps of 128 keys.  `groups`
+// CTA groups share the items; the `tiles` CTAs of a group take one query tile
+// each over the same steps, so that they share their K and V in L2.  What a
+// group does of an item is a piece.  Starting and ending a piece costs a CTA
+// about as much as four steps, so:
+//   few items (at most one to a group): every group gets one piece; an item of s
+//     steps is cut into ceil(s / L) even ones, L the least for which the groups suffice;
+//   more items: their steps in order form one stream, cut into `groups` equal
+//     ranges, where a cut within kSnap steps of an item's end moves there.
+// The pieces of a cut item leave partial results, which are joined.  The cut
+// depends on the lengths alone, so results are the same on every run.
 constexpr int kTreeCtas = 148;  // one CTA on each SM of a B200
+constexpr int kSnap = 4;
 
 ATTN25_HD int tree_groups(int tiles) { return tiles >= kTreeCtas ? 1 : kTreeCtas / tiles; }
 
@@ -91,17 +97,50 @@ ATTN25_HD int item_steps(int len, int n_new, bool has_new) {
   return s > 0 ? s : 1;
 }
 
-ATTN25_HD long long range_start(long long total, int groups, int g) { return total * g / groups; }
-
-// Partial results: group g keeps the piece that begins where its range begins
-// in slot 2 g, and the one that begins inside its range in slot 2 g + 1.
-ATTN25_HD int partial_slot(int g, bool at_range_start) { return 2 * g + (at_range_start ? 0 : 1); }
-
-// Whether the boundary before group g (1 <= g < groups) is the first inside
-// the item [i0, i1): the block of that boundary joins the item.
-ATTN25_HD bool joins_item(long long total, int groups, int g, long long i0, long long i1) {
-  const long long at = range_start(total, groups, g);
-  return at > i0 && at < i1 && range_start(total, groups, g - 1) <= i0;
+// floor(x y / z), x y below 2^63 (in 32 bits where it fits: y is at most 148)
+ATTN25_HD long long mul_div(long long x, int y, long long z) {
+  if (x < (1 << 24) && z < (1 << 24)) return static_cast<uint32_t>(x) * static_cast<uint32_t>(y) / static_cast<uint32_t>(z);
+  return x * y / z;
 }
+
+// Steps [begin, end) of the k-th of n even pieces of an item of s steps.
+ATTN25_HD int even_cut(int s, int k, int n) { return static_cast<int>(mul_div(s, k, n)); }
+
+// The stream's raw cut before group g, and the same moved to the end of the
+// item [i0, i1) that holds it if that is near.
+ATTN25_HD long long raw_cut(long long total, int groups, int g) { return mul_div(total, g, groups); }
+ATTN25_HD long long snapped(long long at, long long i0, long long i1) {
+  if (at - i0 < kSnap) return i0;
+  return i1 - at < kSnap ? i1 : at;
+}
+
+// The cuts that stay inside the item [i0, i1): those before the groups first,
+// first + 1, ..., first + count - 1.
+struct InnerCuts {
+  int first, count;
+};
+ATTN25_HD InnerCuts inner_cuts(long long total, int groups, long long i0, long long i1) {
+  InnerCuts c;
+  // raw_cut(g) >= x  <=>  g >= x groups / total
+  const long long a = i0 + kSnap, z = i1 - kSnap + 1;
+  c.first = static_cast<int>(mul_div(a, groups, total));
+  while (raw_cut(total, groups, c.first) < a) ++c.first;
+  int end = z > 0 ? static_cast<int>(mul_div(z, groups, total)) : 0;
+  while (raw_cut(total, groups, end) < z) ++end;
+  if (c.first < 1) c.first = 1;
+  if (end > groups) end = groups;
+  c.count = end > c.first ? end - c.first : 0;
+  return c;
+}
+
+// Partial results of a cut item of the stream: the piece from the cut before
+// group g in slot 2 g, the piece from the item's begin in the slot before its
+// first inner cut's.  (Few items: a group's piece in the slot of its number.)
+ATTN25_HD int slot_from_cut(int g) { return 2 * g; }
+ATTN25_HD int slot_from_begin(int first_cut) { return 2 * first_cut - 1; }
+
+// The counters of the pieces written, one to a cut item (known by the group of
+// its first inner cut, or of its first piece), lie at the head of the workspace.
+constexpr int kTreeCounterBytes = 1024;
 
 }  // namespace attn25

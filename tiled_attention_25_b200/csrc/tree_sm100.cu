@@ -7,28 +7,35 @@
 // ~2800 clocks in which HBM delivers its 64 KB of K and V to one SM (its 148th
 // share), so the kernel is a stream of K and V: what counts is that every SM
 // has an equal share of the bytes of all rows, whatever their lengths, and
-// always enough copies in flight (192 KB of rings).
+// always enough copies in flight (160 KB or more of rings).
 //
 // Work: the steps of all (row, KV head) items form one stream that is cut into
-// equal ranges (cache_index.h), one CTA per SM.  Items cut by a range boundary
-// leave (m, l, O) partials in fp32, which tree_join_kernel joins; the others
-// are written out directly.
+// equal ranges (cache_index.h), one CTA per SM.  The pieces of an item cut by a
+// range boundary leave (m, l, O) partials in fp32, and the CTA that writes the
+// last of them joins them (a second launch for the joins took 4 to 12 us more);
+// the other items are written out directly.
 //
-// Warp roles (384 threads, as in the forward kernel):
-//   warps 0-3  softmax of the even steps of a piece (thread = query row)
+// Warp roles (384 threads):
+//   warps 0-3  softmax of the even steps of a piece
 //   warps 4-7  softmax of the odd steps
 //   warp  8    MMA issuer
-//   warp  9    TMA producer of Q and K: walks the ranges, publishes the pieces
-//   warp 10    TMA producer of V
-// (One producer for both rings held the stream up: a 128-key copy from pages of
-// 64 rows takes a warp ~1400 clocks of page lookups and issue, and HBM delivers
-// one every 1400.)
-// The two softmax warpgroups keep separate (m, l, O) of the same rows, so that
-// one's softmax runs under the other's products; both are joined at the end of
-// a piece.  Each running maximum moves only when exceeded by more than 2^8, as
-// in the forward kernel.  P is rounded to bf16 for the PV product (half a step,
-// 2^-8 relative, the forward kernel's choice: the product then runs at the full
-// bf16 rate straight from tensor memory); sums, maxima and O stay in fp32.
+//   warp  9    walks the ranges, publishes the pieces, loads K
+//   warps 10, 11  load V, and Q
+// (One producer for all held the stream up: a 128-key copy from pages of 64 rows
+// takes a warp ~1400 clocks of page lookups and issue, and HBM delivers one
+// every 1400.)
+//
+// Few rows would leave three of the four lane quarters, and their warps, idle
+// while one warp works through 128 scores a row in ~3000 clocks.  So a tile of
+// up to 32 (64) rows is loaded 4 (2) times over, S comes out R = 4 (2) times,
+// and each copy's warps take 128 / R of the step's keys: P is zero elsewhere in
+// their lanes, and every copy keeps its own (m, l, O) of its keys.  Together
+// with the two warpgroups, 2 R states of a row are joined at the end of a
+// piece, through shared memory.  Each running maximum moves only when exceeded
+// by more than 2^8, as in the forward kernel.  P is rounded to bf16 for the PV
+// product (half a step, 2^-8 relative, the forward kernel's choice: the product
+// then runs at the full bf16 rate straight from tensor memory); sums, maxima
+// and O stay in fp32.
 //
 // Keys a row does not see are masked by selection before the softmax, so K
 // may hold anything there; V rows behind the last valid key of a step are
@@ -49,19 +56,19 @@ namespace {
 
 constexpr int kTreeThreads = 384;
 constexpr float kTreeRescale = 8.0f;
-// Where a tile has at most 64 rows, two Q tiles share one tile's room (rows 0
-// and 64 of it), so that the next piece's Q need not wait for this piece's last
-// product; that product's rows from 64 on then read whatever follows.
-constexpr int kQBufBytes = 64 * 128;
+constexpr int kStageCols = 16;  // columns of O joined at a time
 
 template <int D>
 struct TreeCfg {
   static constexpr int kTileBytes = TILE * D * 2;
-  // a ring each for K and V: 96 + 96 KB
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  // a ring each for K and V (96 + 64 KB, or 96 + 80), and 32 KB in which the
+  // states of a row are joined: two buffers of 128 rows x 16 columns a warpgroup
+  static constexpr int kKStages = D == 128 ? 3 : 6;
+  static constexpr int kVStages = D == 128 ? 2 : 5;
   static constexpr int kKOff = kTileBytes;  // after Q
-  static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr int kStageOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kBarOff = kStageOff + 4 * TILE * kStageCols * 4;
   static constexpr int kSmemBytes = kBarOff + 1024;
   static constexpr int kAllocBytes = kSmemBytes + 1024;  // + alignment slack
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, false, true);
@@ -72,22 +79,25 @@ struct Piece {
   int32_t b, hk, j0, n;     // b < 0: the end
   int32_t len, n_new;       // filled slots and new tokens of the row
   int32_t slot;             // partial-result slot, or -1: the whole item
+  // of a cut item: its pieces, the slots of the first, the second, and from one
+  // to the next, and its counter
+  int32_t pieces, slot0, slot1, slot_step, counter;
 };
 
 struct TreeBarriers {
   uint64_t list_full[2], list_empty[2];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t o_final, s_free, epi_done;
-  uint64_t ml_ready[4];  // the two warps of a lane quarter have exchanged (m, l)
+  uint64_t o_final, ml_ready, staged[2], epi_done, written, counted;
+  int32_t last;  // this CTA's piece is the last of its item to be written
   uint64_t drain;
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t k_full[6], k_empty[6], v_full[5], v_empty[5];
   uint32_t tmem_base, abort_flag, never_set;
   Piece piece[2];
 };
 static_assert(sizeof(TreeBarriers) <= 1024, "barrier block");
 
-constexpr int kListReaders = 10;  // the MMA warp, the V producer and the 8 softmax warps (lane 0 each)
+constexpr int kListReaders = 11;  // the MMA warp, the V and Q producers and the 8 softmax warps (lane 0 each)
 
 // A place in a ring.
 template <int STAGES>
@@ -115,6 +125,7 @@ struct TreeParams {
   TreeArgs a;
   RowTiles rt;
   int groups;
+  int* counters;   // [group][tile]: pieces written of a cut item
   float* part_o;   // [slot][tile][rows][D]
   float2* part_ml; // [slot][tile][rows]
   uint64_t wait_ns;
@@ -123,7 +134,7 @@ struct TreeParams {
   // (exact: step and page_steps are at most 8192)
   int page_lg, page_steps;
   uint32_t page_magic;
-  int q_bufs;  // 2 where two Q tiles fit one tile's room (up to 64 rows)
+  uint32_t head_magic;  // row / head_tile = row * head_magic >> 16 (rows below 128)
 };
 
 // The stream of items as a warp walks it: 32 rows' lengths at a time, one to a lane.
@@ -145,34 +156,38 @@ __device__ __forceinline__ void scan_load(RowScan& s, const TreeArgs& a, int bas
   if (bad) flag_index(a.c.status);
 }
 
-// Steps of the stream (all rows and heads).  `s` is left at the first window.
-__device__ __forceinline__ long long scan_total(RowScan& s, const TreeArgs& a) {
-  long long total = 0;
-  scan_load(s, a, 0);
-  total = s.steps;
+// Sum over all rows of f(steps of the row's items); `s` is left at the first window.
+template <class F>
+__device__ __forceinline__ long long scan_sum(RowScan& s, const TreeArgs& a, F f) {
+  if (s.base != 0) scan_load(s, a, 0);
+  if (a.c.ix.B <= 32) return __reduce_add_sync(0xffffffffu, static_cast<unsigned>(f(s.steps)));
+  long long sum = f(s.steps);
   for (int base = 32; base < a.c.ix.B; base += 32) {
     RowScan w;
     scan_load(w, a, base);
-    total += w.steps;
+    sum += f(w.steps);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return total * a.c.ix.Hkv;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
 }
 
-// Find the row that holds stream position `at` (< total): its index, the
-// position of its first step, its lengths and its steps per head.
+// Find the row that holds position `at` of a stream in which each of a row's
+// items takes f(its steps) places: its index, the position of its first place,
+// its lengths and its steps per head.
 struct RowAt {
   int b, len, n_new, steps;
   long long start;
 };
 
-__device__ __forceinline__ RowAt scan_find(RowScan& s, const TreeArgs& a, long long at) {
+template <class F>
+__device__ __forceinline__ RowAt scan_find(RowScan& s, const TreeArgs& a, long long at, F f) {
   const int lane = threadIdx.x & 31;
   if (s.base != 0) scan_load(s, a, 0);
   long long before = 0;
   while (true) {
-    long long inc = static_cast<long long>(s.steps) * a.c.ix.Hkv;
+    const long long places = static_cast<long long>(f(s.steps)) * a.c.ix.Hkv;
+    long long inc = places;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -186,7 +201,7 @@ __device__ __forceinline__ RowAt scan_find(RowScan& s, const TreeArgs& a, long l
       r.len = __shfl_sync(0xffffffffu, s.len, l);
       r.n_new = __shfl_sync(0xffffffffu, s.n_new, l);
       r.steps = __shfl_sync(0xffffffffu, s.steps, l);
-      r.start = before + __shfl_sync(0xffffffffu, inc, l) - static_cast<long long>(r.steps) * a.c.ix.Hkv;
+      r.start = before + __shfl_sync(0xffffffffu, inc - places, l);
       return r;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
@@ -211,6 +226,96 @@ __device__ __forceinline__ void scan_next(RowScan& s, const TreeArgs& a, RowAt& 
     scan_load(s, a, s.base + 32);
     from = 0;
   }
+}
+
+// A group's share of the work (cache_index.h).
+struct Walk {
+  RowScan scan;
+  RowAt row;             // the row of the next piece
+  long long total;       // steps of all items
+  long long at, end;     // more items than groups: what is left of the group's range
+  int parts;             // few items: pieces of the group's item (0: more items than groups)
+  int place;             // and which place of the row's items the group has
+};
+
+__device__ __forceinline__ long long walk_cut(Walk& w, const TreeParams& p, int g) {
+  const auto steps = [](int x) { return x; };
+  if (g == 0) return 0;
+  if (g == p.groups) return w.total;
+  const long long at = raw_cut(w.total, p.groups, g);
+  const RowAt r = scan_find(w.scan, p.a, at, steps);
+  const long long i0 = r.start + (at - r.start) / r.steps * r.steps;
+  return snapped(at, i0, i0 + r.steps);
+}
+
+__device__ __forceinline__ void walk_start(Walk& w, const TreeParams& p, int group) {
+  const TreeArgs& a = p.a;
+  const auto steps = [](int x) { return x; };
+  scan_load(w.scan, a, 0);
+  w.total = scan_sum(w.scan, a, steps) * a.c.ix.Hkv;
+  const long long items = scan_sum(w.scan, a, [](int x) { return x > 0 ? 1 : 0; }) * a.c.ix.Hkv;
+  w.at = w.end = 0;
+  w.parts = 0;
+  if (w.total == 0) return;
+  if (items <= p.groups) {
+    int lo = static_cast<int>((w.total + p.groups - 1) / p.groups), hi = item_steps(a.c.ix.capacity, a.T, a.k_new != nullptr);
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (scan_sum(w.scan, a, [&](int x) { return (x + mid - 1) / mid; }) * a.c.ix.Hkv <= p.groups) hi = mid;
+      else lo = mid + 1;
+    }
+    const auto pieces = [&](int x) { return (x + lo - 1) / lo; };
+    if (group >= scan_sum(w.scan, a, pieces) * a.c.ix.Hkv) return;
+    w.row = scan_find(w.scan, a, group, pieces);
+    w.parts = pieces(w.row.steps);
+    w.place = group - static_cast<int>(w.row.start);
+    return;
+  }
+  w.at = walk_cut(w, p, group);
+  w.end = walk_cut(w, p, group + 1);
+  if (w.at < w.end) w.row = scan_find(w.scan, a, w.at, steps);
+}
+
+// The group's next piece; false at the end.
+__device__ __forceinline__ bool walk_next(Walk& w, const TreeParams& p, int group, Piece& pc) {
+  pc.slot = -1;
+  if (w.parts > 0) {
+    pc.hk = w.place / w.parts;
+    const int k = w.place - pc.hk * w.parts;
+    pc.j0 = even_cut(w.row.steps, k, w.parts);
+    pc.n = even_cut(w.row.steps, k + 1, w.parts) - pc.j0;
+    if (w.parts > 1) {
+      pc.slot = group;
+      pc.pieces = w.parts;
+      pc.slot0 = pc.counter = group - k;
+      pc.slot1 = pc.slot0 + 1;
+      pc.slot_step = 1;
+    }
+    w.parts = 0;
+  } else {
+    if (w.at >= w.end) return false;
+    if (w.at >= w.row.start + static_cast<long long>(w.row.steps) * p.a.c.ix.Hkv) scan_next(w.scan, p.a, w.row);
+    const long long in_row = w.at - w.row.start;
+    pc.hk = static_cast<int>(in_row / w.row.steps);
+    pc.j0 = static_cast<int>(in_row - static_cast<long long>(pc.hk) * w.row.steps);
+    const long long left = w.end - w.at;
+    pc.n = w.row.steps - pc.j0 < left ? w.row.steps - pc.j0 : static_cast<int>(left);
+    if (pc.n < w.row.steps) {
+      const long long i0 = w.at - pc.j0;
+      const InnerCuts c = inner_cuts(w.total, p.groups, i0, i0 + w.row.steps);
+      pc.pieces = c.count + 1;
+      pc.slot0 = slot_from_begin(c.first);
+      pc.slot1 = slot_from_cut(c.first);
+      pc.slot_step = slot_from_cut(1);
+      pc.counter = c.first;
+      pc.slot = pc.j0 == 0 ? pc.slot0 : slot_from_cut(group);
+    }
+    w.at += pc.n;
+  }
+  pc.b = w.row.b;
+  pc.len = w.row.len;
+  pc.n_new = w.row.n_new;
+  return true;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -295,22 +400,10 @@ __device__ __forceinline__ uint4 ancestor_bits(const TreeArgs& a, int b, int t, 
   return w;
 }
 
-__device__ __forceinline__ void tmem_st2(uint32_t taddr, float x, float y) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(__float_as_uint(x)),
-               "r"(__float_as_uint(y))
-               : "memory");
-}
-__device__ __forceinline__ float2 tmem_ld2(uint32_t taddr) {
-  uint32_t x, y;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(taddr));
-  tmem_wait_ld();
-  return make_float2(__uint_as_float(x), __uint_as_float(y));
-}
-
 // Copy one of a piece's tensors (K or V) into its ring, step by step.
-template <int D>
+template <int D, int STAGES>
 __device__ __forceinline__ bool produce(const TreeParams& p, const Piece& pc, const CUtensorMap* pool, const CUtensorMap* fresh,
-                                        uint32_t ring, uint64_t* full, uint64_t* empty, RingPos<TreeCfg<D>::kStages>& pos,
+                                        uint32_t ring, uint64_t* full, uint64_t* empty, RingPos<STAGES>& pos,
                                         uint32_t& copies, const WaitCtl& wc) {
   const TreeArgs& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -386,7 +479,96 @@ __device__ __forceinline__ int step_keys(const TreeArgs& a, const Piece& pc, int
   return a.k_new != nullptr ? min(TILE, pc.n_new - (step - n_prefix) * TILE) : 0;
 }
 
-template <int D, bool SOFTCAP>
+__device__ __forceinline__ int row_token(const TreeParams& p, int r) { return static_cast<int>(r * p.head_magic >> 16); }
+
+// Quad (four columns) q of lane `lane` in a 128 x 16 staging buffer: the quads
+// of a lane are rotated so that eight lanes' 16-byte accesses, whether one quad
+// of eight lanes or all quads of two, fall into 32 banks.
+__device__ __forceinline__ int stage_quad(int lane, int q) { return lane * 4 + ((q + (lane >> 1)) & 3); }
+
+// Join the pieces of an item, by the CTA that wrote the last of them: a warp
+// takes NR rows at a time, its lanes their columns, and reads NP pieces ahead
+// (what it costs is the latency of the partials in L2).  The order is that of
+// the pieces whichever of them came last, so the result does not depend on it.
+template <int D, int NR, int NP>
+__device__ __forceinline__ void join_rows(const TreeParams& p, const Piece& pc, int tile, int t0, int h0) {
+  constexpr int kCols = D / 32;  // of a lane
+  const TreeArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = pc.pieces;
+#pragma unroll 1
+  for (int r0 = warp; r0 < p.rt.rows; r0 += 8 * NR) {
+    float m[NR], l[NR], o[NR][kCols];
+    int row[NR];
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+      row[y] = min(r0 + 8 * y, p.rt.rows - 1);  // (rows behind the tile's read its last row)
+      m[y] = -INFINITY;
+      l[y] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kCols; ++d) o[y][d] = 0.f;
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += NP) {
+      float2 ml[NP][NR];
+      float v[NP][NR][kCols];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int x = min(i0 + i, n - 1), slot = x == 0 ? pc.slot0 : pc.slot1 + (x - 1) * pc.slot_step;
+        const int base = (slot * p.rt.tiles + tile) * p.rt.rows;
+#pragma unroll
+        for (int y = 0; y < NR; ++y) {
+          const int part = base + row[y];  // below 2 x 148 x 128
+          ml[i][y] = __ldcg(p.part_ml + part);
+          if constexpr (kCols == 4) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(p.part_o + part * D) + lane);
+            v[i][y][0] = u.x, v[i][y][1] = u.y, v[i][y][2] = u.z, v[i][y][3] = u.w;
+          } else {
+            const float2 u = __ldcg(reinterpret_cast<const float2*>(p.part_o + part * D) + lane);
+            v[i][y][0] = u.x, v[i][y][1] = u.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < NR; ++y) {
+        float top = m[y];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) top = fmaxf(top, ml[i][y].x);  // (the last piece may be read twice)
+        const float f = m[y] == -INFINITY ? 0.f : ex2_approx(m[y] - top);
+        m[y] = top;
+        l[y] *= f;
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) o[y][d] *= f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const float w = i0 + i < n && ml[i][y].x != -INFINITY ? ex2_approx(ml[i][y].x - top) : 0.f;
+          l[y] = fmaf(w, ml[i][y].y, l[y]);
+#pragma unroll
+          for (int d = 0; d < kCols; ++d) o[y][d] = fmaf(w, v[i][y][d], o[y][d]);
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+      const int r = r0 + 8 * y, r_tok = row_token(p, r), tok = t0 + r_tok, head = h0 + r - r_tok * p.rt.head_tile;
+      if (r >= p.rt.rows || head >= a.G || tok >= pc.n_new) continue;
+      const float inv = l[y] > 0.f ? 1.f / l[y] : 0.f;
+      uint32_t* orow = reinterpret_cast<uint32_t*>(a.out + pc.b * a.o_st.b + (pc.hk * a.G + head) * a.o_st.h + tok * a.o_st.s);
+#pragma unroll
+      for (int d = 0; d < kCols; d += 2) orow[lane * (kCols / 2) + d / 2] = pack_bf16x2(o[y][d] * inv, o[y][d + 1] * inv);
+      if (lane == 0 && a.lse != nullptr)
+        a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] =
+            l[y] > 0.f ? (m[y] + log2f(l[y])) * LN2 : -INFINITY;
+    }
+  }
+}
+
+template <int D>
+__device__ __noinline__ void join_pieces(const TreeParams& p, const Piece& pc, int tile, int t0, int h0) {
+  if (p.rt.rows <= 8) join_rows<D, 1, 8>(p, pc, tile, t0, h0);
+  else join_rows<D, 4, 2>(p, pc, tile, t0, h0);
+}
+
+template <int D, int R, bool SOFTCAP>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
@@ -407,20 +589,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->list_full[i]), 1);
       mbar_init(smem_u32(&bars->list_empty[i]), kListReaders);
-      mbar_init(smem_u32(&bars->q_full[i]), 1);
-      mbar_init(smem_u32(&bars->q_empty[i]), 1);
+      mbar_init(smem_u32(&bars->staged[i]), 4);
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       mbar_init(smem_u32(&bars->p_full[i]), 128);
       mbar_init(smem_u32(&bars->o_full[i]), 1);
     }
+    mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_empty), 1);
     mbar_init(smem_u32(&bars->o_final), 1);
-    mbar_init(smem_u32(&bars->s_free), 8);
+    mbar_init(smem_u32(&bars->ml_ready), 8);
+    mbar_init(smem_u32(&bars->written), 8);
+    mbar_init(smem_u32(&bars->counted), 1);
     mbar_init(smem_u32(&bars->epi_done), 8);
     mbar_init(smem_u32(&bars->drain), 1);
-    for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&bars->ml_ready[w]), 2);
-    for (int s = 0; s < Cfg::kStages; ++s) {
+    for (int s = 0; s < Cfg::kKStages; ++s) {
       mbar_init(smem_u32(&bars->k_full[s]), 1);
       mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    }
+    for (int s = 0; s < Cfg::kVStages; ++s) {
       mbar_init(smem_u32(&bars->v_full[s]), 1);
       mbar_init(smem_u32(&bars->v_empty[s]), 1);
     }
@@ -438,46 +624,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   // the walk's lookups run under the set-up of the other warps
-  RowScan scan{};
-  RowAt row{};
-  long long total = 0, at = 0, end = 0;
-  if (warp == 9) {
-    total = scan_total(scan, a);
-    at = range_start(total, p.groups, group);
-    end = range_start(total, p.groups, group + 1);
-    if (at < end) row = scan_find(scan, a, at);
-  }
+  Walk walk{};
+  if (warp == 9) walk_start(walk, p, group);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may start and wait
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{p.wait_ns, smem_u32(&bars->abort_flag), a.c.status};
 
   if (warp >= 8) {
     if (warp == 9) {
-      // ---------------------------------------------------------- walk, Q and K
-      RingPos<Cfg::kStages> pos;
+      // ---------------------------------------------------------- walk and K
+      RingPos<Cfg::kKStages> pos;
       uint32_t copies = 0;
       int n_pieces = 0;
       bool ok = true;
       while (ok) {
         Piece pc{};
-        pc.b = -1;
-        if (at < end) {
-          if (at >= row.start + static_cast<long long>(row.steps) * a.c.ix.Hkv) scan_next(scan, a, row);
-          const long long in_row = at - row.start;
-          pc.hk = static_cast<int>(in_row / row.steps);
-          pc.j0 = static_cast<int>(in_row - static_cast<long long>(pc.hk) * row.steps);
-          const long long left = end - at;
-          pc.n = row.steps - pc.j0 < left ? row.steps - pc.j0 : static_cast<int>(left);
-          pc.slot = pc.n == row.steps ? -1 : partial_slot(group, at == range_start(total, p.groups, group));
-          at += pc.n;
-          if (t0 >= row.n_new) continue;  // none of the tile's tokens exist in this row
-          pc.b = row.b;
-          pc.len = row.len;
-          pc.n_new = row.n_new;
-        }
+        if (!walk_next(walk, p, group, pc)) pc.b = -1;
+        else if (t0 >= pc.n_new) continue;  // none of the tile's tokens exist in this row
         const int buf = n_pieces & 1;
         if (!tree_wait(smem_u32(&bars->list_empty[buf]), ((n_pieces >> 1) & 1) ^ 1, wc)) { ok = false; break; }
         if (lane == 0) {
@@ -486,32 +651,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         __syncwarp();
         if (pc.b < 0) break;
-        // Q: free once the products of the last piece that used the buffer have read it
-        const int qb = p.q_bufs == 2 ? n_pieces & 1 : 0, q_use = p.q_bufs == 2 ? n_pieces >> 1 : n_pieces;
-        if (!tree_wait(smem_u32(&bars->q_empty[qb]), (q_use & 1) ^ 1, wc)) { ok = false; break; }
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&bars->q_full[qb]);
-          mbar_arrive_expect_tx(bar, p.rt.rows * D * 2);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(q_smem + qb * kQBufBytes + c * (TILE * 128), &tm_q, bar, c * 64, pc.hk * a.G + h0, t0, pc.b);
-        }
-        __syncwarp();
         ++n_pieces;
         ok = produce<D>(p, pc, &tm_k, &tm_kn, k_ring, bars->k_full, bars->k_empty, pos, copies, wc);
       }
-      if (lane == 0) {
-        const WaitCtl drain_wc{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status};
-        drain_ring<Cfg::kStages>(bars->k_full, copies, drain_wc);
-        for (int s = 0; s < p.q_bufs; ++s) {
-          const int uses = p.q_bufs == 2 ? (n_pieces + 1 - s) / 2 : n_pieces;
-          if (uses > 0) mbar_wait_thread(smem_u32(&bars->q_full[s]), (uses - 1) & 1, drain_wc);
-        }
-      }
-    } else if (warp == 10) {
-      // ---------------------------------------------------------- V
-      RingPos<Cfg::kStages> pos;
-      uint32_t copies = 0;
+      if (lane == 0)  // let the copies in flight land before the CTA exits
+        drain_ring<Cfg::kKStages>(bars->k_full, copies,
+                                  WaitCtl{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status});
+    } else if (warp >= 10) {
+      // ---------------------------------------------------------- V (warp 10), Q (warp 11)
+      RingPos<Cfg::kVStages> pos;
+      uint32_t copies = 0, q_loads = 0;
       bool ok = true;
       for (int it = 0; ok; ++it) {
         const int buf = it & 1;
@@ -520,14 +669,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->list_empty[buf]));
         if (pc.b < 0) break;
-        ok = produce<D>(p, pc, &tm_v, &tm_vn, v_ring, bars->v_full, bars->v_empty, pos, copies, wc);
+        if (warp == 10) {
+          ok = produce<D>(p, pc, &tm_v, &tm_vn, v_ring, bars->v_full, bars->v_empty, pos, copies, wc);
+        } else {
+          // free once the last piece's scores are formed; R copies
+          if (!tree_wait(smem_u32(&bars->q_empty), (it & 1) ^ 1, wc)) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&bars->q_full);
+            mbar_arrive_expect_tx(bar, R * p.rt.rows * D * 2);
+            for (int x = 0; x < R; ++x)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(q_smem + c * (TILE * 128) + x * (TILE / R * 128), &tm_q, bar, c * 64, pc.hk * a.G + h0, t0, pc.b);
+          }
+          __syncwarp();
+          ++q_loads;
+        }
       }
-      if (lane == 0)
-        drain_ring<Cfg::kStages>(bars->v_full, copies,
-                                 WaitCtl{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status});
+      if (lane == 0) {
+        const WaitCtl drain_wc{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status};
+        drain_ring<Cfg::kVStages>(bars->v_full, copies, drain_wc);
+        if (q_loads > 0) mbar_wait_thread(smem_u32(&bars->q_full), (q_loads - 1) & 1, drain_wc);
+      }
     } else if (warp == 8) {
       // ---------------------------------------------------------- MMA issuer
-      RingPos<Cfg::kStages> kp, vp;
+      RingPos<Cfg::kKStages> kp;
+      RingPos<Cfg::kVStages> vp;
       uint32_t p_cnt[2] = {0, 0};
       bool ok = true;
       for (int it = 0; ok; ++it) {
@@ -535,11 +702,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (!tree_wait(smem_u32(&bars->list_full[buf]), (it >> 1) & 1, wc)) break;
         const Piece pc = bars->piece[buf];
         if (pc.b < 0) break;
-        const int qb = p.q_bufs == 2 ? it & 1 : 0, q_use = p.q_bufs == 2 ? it >> 1 : it;
-        const uint32_t q = q_smem + qb * kQBufBytes;
-        // the columns of the scores, in which the last piece's (m, l) were exchanged, are free
-        if (!tree_wait(smem_u32(&bars->s_free), (it & 1) ^ 1, wc)) break;
-        if (!tree_wait(smem_u32(&bars->q_full[qb]), q_use & 1, wc)) break;
+        if (!tree_wait(smem_u32(&bars->q_full), it & 1, wc)) break;
         tc_fence_after();
         // S(0) S(1) | O(0) S(2) | O(1) S(3) | ... | O(n-1).  A step's products take
         // only as many of its keys (S columns, rows of V) as exist, in 16s.
@@ -575,16 +738,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (kk >> 2) * (TILE * 128) + (kk & 3) * 32;
-              mma_ss_w(tmem + t * 128, smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k_smem + off, 16, 1024), idesc,
+              mma_ss_w(tmem + t * 128, smem_desc_sw128(q_smem + off, 16, 1024), smem_desc_sw128(k_smem + off, 16, 1024), idesc,
                        kk > 0 ? 1u : 0u);
             }
             mma_commit_w(smem_u32(&bars->s_full[t]));
             mma_commit_w(smem_u32(&bars->k_empty[kp.slot]));
+            if (i == pc.n - 1) mma_commit_w(smem_u32(&bars->q_empty));
             kp.next();
           }
         }
         if (!ok) break;
-        mma_commit_w(smem_u32(&bars->q_empty[qb]));
         mma_commit_w(smem_u32(&bars->o_final));
         if (lane == 0) mbar_arrive(smem_u32(&bars->list_empty[buf]));
         __syncwarp();
@@ -594,15 +757,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
-    const int t = warp >> 2;
-    const int r = threadIdx.x & 127;
+    const int t = warp >> 2, tid = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + t * 128 + lane_off, o_addr = tmem + 256 + t * D + lane_off;
-    const int tok = t0 + r / p.rt.head_tile, head = h0 + r % p.rt.head_tile;
+    // this lane's query row, and the 32-key chunks [c0, c0 + kChunks) of a step that its copy takes
+    constexpr int kChunks = 4 / R;
+    const int r = tid & (TILE / R - 1), copy = tid / (TILE / R), c0 = copy * kChunks;
+    const int r_tok = row_token(p, r), tok = t0 + r_tok, head = h0 + r - r_tok * p.rt.head_tile;
     const bool in_tile = r < p.rt.rows && head < a.G;
+    float4* stage = reinterpret_cast<float4*>(smem + Cfg::kStageOff) + t * 2 * TILE * 4;  // two buffers
     const float sl2 = a.scale * LOG2E;
     const float cap_in = SOFTCAP ? a.scale / a.softcap : 0.f, cap_out = SOFTCAP ? a.softcap * LOG2E : 0.f;
-    uint32_t s_cnt = 0, p_cnt = 0, v_base = 0;  // v_base: V copies before the piece
+    uint32_t s_cnt = 0, p_cnt = 0, v_base = 0, rounds = 0, cuts = 0;  // v_base: V copies before the piece
     for (int it = 0;; ++it) {
       const int buf = it & 1;
       if (!tree_wait(smem_u32(&bars->list_full[buf]), (it >> 1) & 1, wc)) break;
@@ -618,7 +784,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int step = pc.j0 + j;
         const int x0 = (step - n_prefix) * TILE;  // new tokens: first of the step
         // keys of the step that exist, and those this row sees
-        const int n_keys = step_keys(a, pc, step), chunks = (max(n_keys, 1) + 31) / 32;
+        const int n_keys = step_keys(a, pc, step), chunks = (max(n_keys, 1) + 31) / 32;  // chunks the product takes
         const bool partial = n_keys < TILE || step >= n_prefix;
         uint4 keep = first_bits(n_keys);
         if (step >= n_prefix) keep = valid && n_keys > 0 ? ancestor_bits(a, pc.b, tok, x0) : make_uint4(0u, 0u, 0u, 0u);
@@ -626,25 +792,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ++s_cnt;
         tc_fence_after();
         if (busy) {
-          // Two passes over the scores in tensor memory, 32 at a time with the next
-          // 32 on their way: a loop body small enough for the instruction cache
-          // (128 scores in registers, fully unrolled, took twice as long).
-          float xa[32], xb[32], mx = -INFINITY;
-          tmem_ld32(s_addr, reinterpret_cast<uint32_t(&)[32]>(xa));
-#pragma unroll 1
-          for (int c = 0; c < chunks; c += 2) {
-            tmem_wait_ld();
-            if (c + 1 < chunks) tmem_ld32(s_addr + (c + 1) * 32, reinterpret_cast<uint32_t(&)[32]>(xb));
-            chunk_scores<SOFTCAP>(xa, partial, word_of(keep, c), cap_in, cap_out);
-            mx = chunk_max(xa, mx);
-            if (c + 1 < chunks) {
-              tmem_wait_ld();
-              if (c + 2 < chunks) tmem_ld32(s_addr + (c + 2) * 32, reinterpret_cast<uint32_t(&)[32]>(xa));
-              chunk_scores<SOFTCAP>(xb, partial, word_of(keep, c + 1), cap_in, cap_out);
-              mx = chunk_max(xb, mx);
+          float x[kChunks][32], mx = -INFINITY;
+          const int mine = min(kChunks, chunks - c0);  // chunks of this copy that hold keys
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < mine) tmem_ld32(s_addr + (c0 + c) * 32, reinterpret_cast<uint32_t(&)[32]>(x[c]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < mine) {
+              chunk_scores<SOFTCAP>(x[c], partial, word_of(keep, c0 + c), cap_in, cap_out);
+              mx = chunk_max(x[c], mx);
             }
-          }
-          tmem_ld32(s_addr, reinterpret_cast<uint32_t(&)[32]>(xa));  // for the second pass
           if (!SOFTCAP) mx *= sl2;  // -inf stays -inf (sl2 > 0)
           const float m_new = fmaxf(m_run, mx);
           const bool need = m_new > m_run + kTreeRescale;
@@ -668,32 +827,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           const float m_use = m_run == -INFINITY ? 0.f : m_run;
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // P of chunk c lands in columns 16 c .. 16 c + 15, scores already read
-#pragma unroll 1
-          for (int c = 0; c < chunks; c += 2) {
-            tmem_wait_ld();
-            if (c + 1 < chunks) tmem_ld32(s_addr + (c + 1) * 32, reinterpret_cast<uint32_t(&)[32]>(xb));
-            chunk_scores<SOFTCAP>(xa, partial, word_of(keep, c), cap_in, cap_out);
-            if (c + 1 < chunks) {
-              chunk_probs<SOFTCAP>(xa, sl2, m_use, s_addr + c * 16, acc);
-              tmem_wait_ld();
-              if (c + 2 < chunks) tmem_ld32(s_addr + (c + 2) * 32, reinterpret_cast<uint32_t(&)[32]>(xa));
-              chunk_scores<SOFTCAP>(xb, partial, word_of(keep, c + 1), cap_in, cap_out);
-              chunk_probs<SOFTCAP>(xb, sl2, m_use, s_addr + (c + 1) * 16, acc);
-            } else {
-              chunk_probs<SOFTCAP>(xa, sl2, m_use, s_addr + c * 16, acc);
-            }
+          // P of chunk c lands in columns 16 c .. 16 c + 15 (all scores of this warp's
+          // lanes are read); the other copies' keys are zero in these lanes
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < mine) chunk_probs<SOFTCAP>(x[c], sl2, m_use, s_addr + (c0 + c) * 16, acc);
+          if constexpr (R > 1) {
+            const uint32_t zero[16] = {};
+            for (int c = 0; c < chunks; ++c)
+              if (c < c0 || c >= c0 + kChunks) tmem_st16(s_addr + c * 16, zero);
           }
           l_run += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
           tmem_wait_st();
         }
         if (n_keys < TILE) {
           // V rows of no key, up to the last the product takes: zeros, whatever lies there
-          const uint32_t pos = v_base + j, slot = pos % Cfg::kStages;
-          if (!tree_wait(smem_u32(&bars->v_full[slot]), (pos / Cfg::kStages) & 1, wc)) { ok = false; break; }
+          const uint32_t pos = v_base + j, slot = pos % Cfg::kVStages;
+          if (!tree_wait(smem_u32(&bars->v_full[slot]), (pos / Cfg::kVStages) & 1, wc)) { ok = false; break; }
           uint8_t* v = smem + Cfg::kVOff + slot * Cfg::kTileBytes;
           const int rows = (max(n_keys, 1) + 15) / 16 * 16 - n_keys;
-          for (int i = r; i < rows * (D / 8); i += 128) {  // 16-byte chunks; whole rows, so the swizzle does not matter
+          for (int i = tid; i < rows * (D / 8); i += 128) {  // 16-byte chunks; whole rows, so the swizzle does not matter
             const int row = n_keys + i / (D / 8), ch = i % (D / 8);
             *reinterpret_cast<uint4*>(v + (ch >> 3) * (TILE * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -705,67 +858,116 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       if (!ok) break;
       v_base += pc.n;
-      // ---- end of the piece: join the even and the odd steps
+      // ---- end of the piece: join the states of each row, 2 warpgroups x R copies.
+      // Both warpgroups' (m, l) go into both warpgroups' first buffer, so that each
+      // reads its own only.
       if (!tree_wait(smem_u32(&bars->o_final), it & 1, wc)) break;
       tc_fence_after();
-      const uint32_t other_s = tmem + (1 - t) * 128 + lane_off;
-      tmem_st2(s_addr, m_run, l_run);
-      tmem_wait_st();
-      tc_fence_before();
+      float2* ml = reinterpret_cast<float2*>(smem + Cfg::kStageOff);
+      constexpr int kRegion = 2 * TILE * kStageCols / 2;  // a warpgroup's two buffers, in float2
+      ml[t * TILE + tid] = make_float2(m_run, l_run);
+      ml[kRegion + t * TILE + tid] = make_float2(m_run, l_run);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ml_ready[warp & 3]));
-      if (!tree_wait(smem_u32(&bars->ml_ready[warp & 3]), it & 1, wc)) break;
-      tc_fence_after();
-      const float2 other = tmem_ld2(other_s);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->s_free));
-      if (busy) {
-        const float m0 = t == 0 ? m_run : other.x, m1 = t == 0 ? other.x : m_run;
-        const float l0 = t == 0 ? l_run : other.y, l1 = t == 0 ? other.y : l_run;
-        const float m = fmaxf(m0, m1);
-        const float f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m), f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
-        const float l = f0 * l0 + f1 * l1;
-        const float inv = pc.slot >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-        const float g0 = f0 * inv, g1 = f1 * inv;
-        const long long part = static_cast<long long>(pc.slot) * p.rt.tiles + tile;
-        float* po = p.part_o + (part * p.rt.rows + r) * D + t * (D / 2);
-        __nv_bfloat16* orow = a.out + pc.b * a.o_st.b + (pc.hk * a.G + head) * a.o_st.h + tok * a.o_st.s + t * (D / 2);
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ml_ready));
+      if (!tree_wait(smem_u32(&bars->ml_ready), it & 1, wc)) break;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2 * R; ++x) m = fmaxf(m, ml[t * kRegion + (x & 1) * TILE + r + (x >> 1) * (TILE / R)].x);
+      float g[2];
+#pragma unroll
+      for (int x = 0; x < 2 * R; ++x) {
+        const float2 v = ml[t * kRegion + (x & 1) * TILE + r + (x >> 1) * (TILE / R)];
+        const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - m);
+        l = fmaf(f, v.y, l);
+        if ((x >> 1) == copy) g[x & 1] = f;
+      }
+      if (pc.slot < 0) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        g[0] *= inv;
+        g[1] *= inv;
+      }
+      const long long part = (static_cast<long long>(pc.slot) * p.rt.tiles + tile) * p.rt.rows;
+      if (valid && t == 0 && copy == 0) {
+        if (pc.slot >= 0) p.part_ml[part + r] = make_float2(m, l);
+        else if (a.lse != nullptr)
+          a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] =
+              l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+      }
+      // where this thread writes: rows w_row + 32 x, four columns
+      const int w_row = (warp & 3) * 8 + (lane >> 2), quad = lane & 3;
+      constexpr int kRows = 4 / R;
+      long long to[kRows];  // elements; -1: no such row
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        const int row = w_row + 32 * x, rt = row_token(p, row), w_head = h0 + row - rt * p.rt.head_tile;
+        to[x] = -1;
+        if (row < p.rt.rows && w_head < a.G && t0 + rt < pc.n_new)
+          to[x] = pc.slot >= 0 ? (part + row) * D
+                               : pc.b * a.o_st.b + (pc.hk * a.G + w_head) * a.o_st.h + (t0 + rt) * a.o_st.s;
+      }
+      // O, 16 columns at a time (even rounds in the second buffer): scaled into the
+      // buffer, then summed over the copies and written, coalesced, by the warpgroup
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t o0[32], o1[32];
-          const uint32_t col = t * (D / 2) + c * 32;
-          tmem_ld32(tmem + 256 + lane_off + col, o0);
-          if (pc.n > 1) tmem_ld32(tmem + 256 + D + lane_off + col, o1);
+      for (int k = 0; k < D / 2 / kStageCols; ++k) {
+        float4* sb = stage + ((k & 1) ^ 1) * TILE * 4;
+        if (busy) {
+          uint32_t o0[16], o1[16];
+          tmem_ld16(tmem + 256 + lane_off + t * (D / 2) + k * kStageCols, o0);
+          tmem_ld16(tmem + 256 + D + lane_off + t * (D / 2) + k * kStageCols, o1);
           tmem_wait_ld();
-          float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            // a row whose even (odd) steps kept nothing holds zeros there
-            o[e] = __uint_as_float(o0[e]) * g0;
-            if (pc.n > 1) o[e] = fmaf(__uint_as_float(o1[e]), g1, o[e]);
-          }
-          if (valid) {
-            if (pc.slot >= 0) {
+          for (int q = 0; q < 4; ++q) {
+            float o[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float4*>(po + c * 32)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            } else {
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                reinterpret_cast<uint4*>(orow + c * 32)[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              o[e] = __uint_as_float(o0[4 * q + e]) * g[0];
+              if (pc.n > 1) o[e] = fmaf(__uint_as_float(o1[4 * q + e]), g[1], o[e]);  // (one step: the odd O is stale)
             }
+            sb[stage_quad(tid, q)] = make_float4(o[0], o[1], o[2], o[3]);
           }
         }
-        if (valid && t == 0) {
-          if (pc.slot >= 0) p.part_ml[part * p.rt.rows + r] = make_float2(m, l);
-          else if (a.lse != nullptr)
-            a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] =
-                l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->staged[t]));
+        if (!tree_wait(smem_u32(&bars->staged[t]), rounds & 1, wc)) { ok = false; break; }
+        ++rounds;
+        const int col = t * (D / 2) + k * kStageCols + quad * 4;
+#pragma unroll
+        for (int x = 0; x < kRows; ++x) {
+          float4 v = sb[stage_quad(w_row + 32 * x, quad)];
+#pragma unroll
+          for (int y = 1; y < R; ++y) {
+            const float4 u = sb[stage_quad(w_row + 32 * x + y * (TILE / R), quad)];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+          }
+          if (to[x] >= 0) {
+            if (pc.slot >= 0) *reinterpret_cast<float4*>(p.part_o + to[x] + col) = v;
+            else *reinterpret_cast<uint2*>(a.out + to[x] + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          }
         }
+      }
+      if (!ok) break;
+      if (pc.slot >= 0) {
+        // count this piece in once all warps' parts of it are visible to the device;
+        // whoever counts in last joins the item and leaves the counter at zero
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->written));
+        if (!tree_wait(smem_u32(&bars->written), cuts & 1, wc)) break;
+        if (threadIdx.x == 0) {
+          int* counter = p.counters + pc.counter * p.rt.tiles + tile;
+          const bool last = atomicAdd(counter, 1) == pc.pieces - 1;
+          __threadfence();
+          if (last) *counter = 0;
+          bars->last = last ? 1 : 0;
+          mbar_arrive(smem_u32(&bars->counted));
+        }
+        __syncwarp();
+        if (!tree_wait(smem_u32(&bars->counted), cuts & 1, wc)) break;
+        ++cuts;
+        if (bars->last != 0) join_pieces<D>(p, bars->piece[buf], tile, t0, h0);
       }
       tc_fence_before();
       __syncwarp();
@@ -782,110 +984,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Join the pieces of the items that a range boundary cut: block (boundary,
-// tile, 8 rows), one warp to a row, in the order of the pieces.
-constexpr int kJoinThreads = 256, kJoinRows = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p) {
-  const TreeArgs& a = p.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile = blockIdx.x % p.rt.tiles, g = blockIdx.x / p.rt.tiles + 1;
-  RowScan scan;
-  const long long total = scan_total(scan, a);
-  const long long at = range_start(total, p.groups, g);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
-  if (at >= total) return;
-  const RowAt row = scan_find(scan, a, at);
-  const long long hk = (at - row.start) / row.steps, i0 = row.start + hk * row.steps, i1 = i0 + row.steps;
-  if (!joins_item(total, p.groups, g, i0, i1)) return;
-  const int t0 = tile / p.rt.head_chunks * p.rt.tok_tile, h0 = tile % p.rt.head_chunks * p.rt.head_tile;
-  for (int r = blockIdx.y * kJoinRows + warp; r < min(p.rt.rows, (static_cast<int>(blockIdx.y) + 1) * kJoinRows);
-       r += kJoinThreads / 32) {
-    const int tok = t0 + r / p.rt.head_tile, head = h0 + r % p.rt.head_tile;
-    if (head >= a.G || tok >= row.n_new) continue;
-    // 32 pieces at a time: a lane to each for its (m, l), then their O rows in order
-    float m = -INFINITY, l = 0.f, o[D / 32] = {};
-    for (int x0 = g - 1; x0 < p.groups && range_start(total, p.groups, x0) < i1; x0 += 32) {
-      const int x = x0 + lane;
-      long long part = -1;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (x < p.groups) {
-        const long long s = range_start(total, p.groups, x), e = range_start(total, p.groups, x + 1);
-        if (s < i1 && e > s) {
-          part = (static_cast<long long>(partial_slot(x, s >= i0)) * p.rt.tiles + tile) * p.rt.rows + r;
-          ml = p.part_ml[part];
-        }
-      }
-      float top = ml.x;
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      const float m2 = fmaxf(m, top);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - m2), mine = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
-      float sum = ml.y * mine;
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      m = m2;
-      l = l * f + sum;
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] *= f;
-      uint32_t left = __ballot_sync(0xffffffffu, part >= 0);
-      while (left != 0) {  // four rows' loads at a time
-        float v[4][D / 32], wt[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int src = left != 0 ? __ffs(left) - 1 : 0;
-          const bool any = left != 0;
-          left &= left - 1;
-          const long long from = __shfl_sync(0xffffffffu, part, src);
-          wt[i] = __shfl_sync(0xffffffffu, mine, src);
-          if (!any) wt[i] = 0.f;
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d) v[i][d] = any ? p.part_o[from * D + lane + 32 * d] : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int d = 0; d < D / 32; ++d) o[d] = fmaf(v[i][d], wt[i], o[d]);
-      }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16* orow = a.out + row.b * a.o_st.b + (hk * a.G + head) * a.o_st.h + tok * a.o_st.s;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) orow[lane + 32 * d] = __float2bfloat16(o[d] * inv);
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[(static_cast<long long>(row.b) * a.Hq + hk * a.G + head) * a.T + tok] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
-  }
-}
-
-template <int D, bool SOFTCAP>
+template <int D, int R, bool SOFTCAP>
 cudaError_t launch_tree_t(const TreeMaps& m, const TreeParams& p, cudaStream_t stream) {
-  auto kernel = attn_tree_kernel<D, SOFTCAP>;
+  auto kernel = attn_tree_kernel<D, R, SOFTCAP>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = prepare_kernel(done, kernel, TreeCfg<D>::kAllocBytes, 0);
   if (e != cudaSuccess) return e;
   kernel<<<p.groups * p.rt.tiles, kTreeThreads, TreeCfg<D>::kAllocBytes, stream>>>(m.q, m.k, m.v, m.kn, m.vn, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.groups == 1) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((p.groups - 1) * p.rt.tiles, (p.rt.rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, p);
+  return cudaGetLastError();
+}
+
+// Copies of the query tile: as many as fit its 128 rows, up to 4.
+template <int D, bool SOFTCAP>
+cudaError_t launch_tree_r(const TreeMaps& m, const TreeParams& p, cudaStream_t stream) {
+  if (p.rt.rows <= 32) return launch_tree_t<D, 4, SOFTCAP>(m, p, stream);
+  if (p.rt.rows <= 64) return launch_tree_t<D, 2, SOFTCAP>(m, p, stream);
+  return launch_tree_t<D, 1, SOFTCAP>(m, p, stream);
 }
 
 }  // namespace
+
+static_assert(kTreeCtas * sizeof(int) <= kTreeCounterBytes, "counters");
 
 size_t tree_workspace_bytes(int G, int T, int D) {
   const RowTiles rt = row_tiles(G, T);
   // groups * tiles <= 148 where there is more than one group
   const size_t rows = static_cast<size_t>(2) * kTreeCtas * rt.rows;
-  return (rows * D * 4 + 255) / 256 * 256 + (rows * 8 + 255) / 256 * 256;
+  return kTreeCounterBytes + (rows * D * 4 + 255) / 256 * 256 + (rows * 8 + 255) / 256 * 256;
 }
 
 cudaError_t launch_tree(const TreeMaps& m, const TreeArgs& a, void* workspace, uint64_t wait_ns, cudaStream_t stream) {
@@ -893,17 +1018,19 @@ cudaError_t launch_tree(const TreeMaps& m, const TreeArgs& a, void* workspace, u
   p.a = a;
   p.rt = row_tiles(a.G, a.T);
   p.groups = tree_groups(p.rt.tiles);
-  p.q_bufs = p.rt.rows <= 64 ? 2 : 1;
+  p.head_magic = 65535u / p.rt.head_tile + 1;
   const int ps = a.c.ix.page_size;
   while (ps << p.page_lg < TILE) ++p.page_lg;
   p.page_steps = ps / TILE;
   if (p.page_steps > 1) p.page_magic = static_cast<uint32_t>(((1ull << 32) + p.page_steps - 1) / p.page_steps);
   const size_t rows = static_cast<size_t>(2) * kTreeCtas * p.rt.rows;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + (rows * a.c.D * 4 + 255) / 256 * 256);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.counters = reinterpret_cast<int*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + kTreeCounterBytes);
+  p.part_ml = reinterpret_cast<float2*>(ws + kTreeCounterBytes + (rows * a.c.D * 4 + 255) / 256 * 256);
   p.wait_ns = wait_ns;
-  if (a.c.D == 128) return a.softcap > 0.f ? launch_tree_t<128, true>(m, p, stream) : launch_tree_t<128, false>(m, p, stream);
-  return a.softcap > 0.f ? launch_tree_t<64, true>(m, p, stream) : launch_tree_t<64, false>(m, p, stream);
+  if (a.c.D == 128) return a.softcap > 0.f ? launch_tree_r<128, true>(m, p, stream) : launch_tree_r<128, false>(m, p, stream);
+  return a.softcap > 0.f ? launch_tree_r<64, true>(m, p, stream) : launch_tree_r<64, false>(m, p, stream);
 }
 
 }  // namespace attn25

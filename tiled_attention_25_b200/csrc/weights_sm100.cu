@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     WScan scan;
     w_load(scan, a, 0);
     const long long total = units_below(scan, a, INT_MAX);
-    long long at = range_start(total, gridDim.x, blockIdx.x);
-    const long long end = range_start(total, gridDim.x, blockIdx.x + 1);
+    long long at = raw_cut(total, gridDim.x, blockIdx.x);
+    const long long end = raw_cut(total, gridDim.x, blockIdx.x + 1);
     auto nth = [&](long long u) {  // unit u in the order of the grid's walk
       Unit x;
       if (p.one_tile) {
