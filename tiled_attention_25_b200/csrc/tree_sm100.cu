@@ -258,7 +258,9 @@ __device__ __forceinline__ void walk_start(Walk& w, const TreeParams& p, int gro
   w.parts = 0;
   if (w.total == 0) return;
   if (items <= p.groups) {
+    // sum ceil(s / L) <= total / L + items bounds L from above
     int lo = static_cast<int>((w.total + p.groups - 1) / p.groups), hi = item_steps(a.c.ix.capacity, a.T, a.k_new != nullptr);
+    if (items < p.groups) hi = min(hi, static_cast<int>((w.total + p.groups - items - 1) / (p.groups - items)));
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (scan_sum(w.scan, a, [&](int x) { return (x + mid - 1) / mid; }) * a.c.ix.Hkv <= p.groups) hi = mid;
@@ -565,7 +567,7 @@ __device__ __forceinline__ void join_rows(const TreeParams& p, const Piece& pc, 
 template <int D>
 __device__ __noinline__ void join_pieces(const TreeParams& p, const Piece& pc, int tile, int t0, int h0) {
   if (p.rt.rows <= 8) join_rows<D, 1, 8>(p, pc, tile, t0, h0);
-  else join_rows<D, 4, 2>(p, pc, tile, t0, h0);
+  else join_rows<D, 2, 4>(p, pc, tile, t0, h0);
 }
 
 template <int D, int R, bool SOFTCAP>
@@ -792,18 +794,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         ++s_cnt;
         tc_fence_after();
         if (busy) {
-          float x[kChunks][32], mx = -INFINITY;
+          // at most 64 scores in registers: with all 128 of R = 1 the kernel spills, and
+          // local memory is slow beside 227 KB of shared memory
+          constexpr int kHold = kChunks < 2 ? kChunks : 2;
+          float x[kHold][32], mx = -INFINITY;
           const int mine = min(kChunks, chunks - c0);  // chunks of this copy that hold keys
+          auto load = [&](int from) {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if (c < mine) tmem_ld32(s_addr + (c0 + c) * 32, reinterpret_cast<uint32_t(&)[32]>(x[c]));
-          tmem_wait_ld();
+            for (int c = 0; c < kHold; ++c)
+              if (from + c < mine) tmem_ld32(s_addr + (c0 + from + c) * 32, reinterpret_cast<uint32_t(&)[32]>(x[c]));
+            tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if (c < mine) {
-              chunk_scores<SOFTCAP>(x[c], partial, word_of(keep, c0 + c), cap_in, cap_out);
-              mx = chunk_max(x[c], mx);
-            }
+            for (int c = 0; c < kHold; ++c)
+              if (from + c < mine) chunk_scores<SOFTCAP>(x[c], partial, word_of(keep, c0 + from + c), cap_in, cap_out);
+          };
+#pragma unroll 1
+          for (int from = kChunks - kHold; from >= 0; from -= kHold) {  // the first chunks last: they stay
+            load(from);
+#pragma unroll
+            for (int c = 0; c < kHold; ++c)
+              if (from + c < mine) mx = chunk_max(x[c], mx);
+          }
           if (!SOFTCAP) mx *= sl2;  // -inf stays -inf (sl2 > 0)
           const float m_new = fmaxf(m_run, mx);
           const bool need = m_new > m_run + kTreeRescale;
@@ -827,11 +838,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           const float m_use = m_run == -INFINITY ? 0.f : m_run;
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // P of chunk c lands in columns 16 c .. 16 c + 15 (all scores of this warp's
-          // lanes are read); the other copies' keys are zero in these lanes
+          // P of chunk c lands in columns 16 c .. 16 c + 15, whose scores are read by
+          // then; the other copies' keys are zero in these lanes
+#pragma unroll 1
+          for (int from = 0; from < kChunks; from += kHold) {
+            if (from > 0) load(from);
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if (c < mine) chunk_probs<SOFTCAP>(x[c], sl2, m_use, s_addr + (c0 + c) * 16, acc);
+            for (int c = 0; c < kHold; ++c)
+              if (from + c < mine) chunk_probs<SOFTCAP>(x[c], sl2, m_use, s_addr + (c0 + from + c) * 16, acc);
+          }
           if constexpr (R > 1) {
             const uint32_t zero[16] = {};
             for (int c = 0; c < chunks; ++c)
