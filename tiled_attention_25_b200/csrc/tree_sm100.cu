@@ -158,18 +158,16 @@ __device__ __forceinline__ void scan_load(RowScan& s, const TreeArgs& a, int bas
 
 // Sum over all rows of f(steps of the row's items); `s` is left at the first window.
 template <class F>
-__device__ __forceinline__ long long scan_sum(RowScan& s, const TreeArgs& a, F f) {
+__device__ __forceinline__ int scan_sum(RowScan& s, const TreeArgs& a, F f) {
   if (s.base != 0) scan_load(s, a, 0);
-  if (a.c.ix.B <= 32) return __reduce_add_sync(0xffffffffu, static_cast<unsigned>(f(s.steps)));
-  long long sum = f(s.steps);
+  if (a.c.ix.B <= 32) return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(f(s.steps))));
+  int sum = f(s.steps);
   for (int base = 32; base < a.c.ix.B; base += 32) {
     RowScan w;
     scan_load(w, a, base);
     sum += f(w.steps);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
+  return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(sum)));
 }
 
 // Find the row that holds position `at` of a stream in which each of a row's
@@ -177,20 +175,20 @@ __device__ __forceinline__ long long scan_sum(RowScan& s, const TreeArgs& a, F f
 // its lengths and its steps per head.
 struct RowAt {
   int b, len, n_new, steps;
-  long long start;
+  int start;
 };
 
 template <class F>
-__device__ __forceinline__ RowAt scan_find(RowScan& s, const TreeArgs& a, long long at, F f) {
+__device__ __forceinline__ RowAt scan_find(RowScan& s, const TreeArgs& a, int at, F f) {
   const int lane = threadIdx.x & 31;
   if (s.base != 0) scan_load(s, a, 0);
-  long long before = 0;
+  int before = 0;
   while (true) {
-    const long long places = static_cast<long long>(f(s.steps)) * a.c.ix.Hkv;
-    long long inc = places;
+    const int places = f(s.steps) * a.c.ix.Hkv;
+    int inc = places;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + inc > at);
@@ -211,7 +209,7 @@ __device__ __forceinline__ RowAt scan_find(RowScan& s, const TreeArgs& a, long l
 
 // The next row with steps after row `r.b` (one exists).
 __device__ __forceinline__ void scan_next(RowScan& s, const TreeArgs& a, RowAt& r) {
-  r.start += static_cast<long long>(r.steps) * a.c.ix.Hkv;
+  r.start += r.steps * a.c.ix.Hkv;
   int from = r.b + 1 - s.base;
   while (true) {
     const uint32_t later = from < 32 ? __ballot_sync(0xffffffffu, s.steps > 0) & (0xffffffffu << from) : 0u;
@@ -228,24 +226,25 @@ __device__ __forceinline__ void scan_next(RowScan& s, const TreeArgs& a, RowAt& 
   }
 }
 
-// A group's share of the work (cache_index.h).
+// A group's share of the work (cache_index.h).  Positions fit 32 bits: at most
+// 65535 items of 8200 steps.
 struct Walk {
   RowScan scan;
   RowAt row;             // the row of the next piece
-  long long total;       // steps of all items
-  long long at, end;     // more items than groups: what is left of the group's range
+  int total;             // steps of all items
+  int at, end;           // more items than groups: what is left of the group's range
   int parts;             // few items: pieces of the group's item (0: more items than groups)
   int place;             // and which place of the row's items the group has
 };
 
-__device__ __forceinline__ long long walk_cut(Walk& w, const TreeParams& p, int g) {
+__device__ __forceinline__ int walk_cut(Walk& w, const TreeParams& p, int g) {
   const auto steps = [](int x) { return x; };
   if (g == 0) return 0;
   if (g == p.groups) return w.total;
-  const long long at = raw_cut(w.total, p.groups, g);
+  const int at = static_cast<int>(raw_cut(w.total, p.groups, g));
   const RowAt r = scan_find(w.scan, p.a, at, steps);
-  const long long i0 = r.start + (at - r.start) / r.steps * r.steps;
-  return snapped(at, i0, i0 + r.steps);
+  const int i0 = r.start + (at - r.start) / r.steps * r.steps;
+  return static_cast<int>(snapped(at, i0, i0 + r.steps));
 }
 
 __device__ __forceinline__ void walk_start(Walk& w, const TreeParams& p, int group) {
@@ -253,24 +252,24 @@ __device__ __forceinline__ void walk_start(Walk& w, const TreeParams& p, int gro
   const auto steps = [](int x) { return x; };
   scan_load(w.scan, a, 0);
   w.total = scan_sum(w.scan, a, steps) * a.c.ix.Hkv;
-  const long long items = scan_sum(w.scan, a, [](int x) { return x > 0 ? 1 : 0; }) * a.c.ix.Hkv;
+  const int items = scan_sum(w.scan, a, [](int x) { return x > 0 ? 1 : 0; }) * a.c.ix.Hkv;
   w.at = w.end = 0;
   w.parts = 0;
   if (w.total == 0) return;
   if (items <= p.groups) {
     // sum ceil(s / L) <= total / L + items bounds L from above
-    int lo = static_cast<int>((w.total + p.groups - 1) / p.groups), hi = item_steps(a.c.ix.capacity, a.T, a.k_new != nullptr);
-    if (items < p.groups) hi = min(hi, static_cast<int>((w.total + p.groups - items - 1) / (p.groups - items)));
+    int lo = (w.total + p.groups - 1) / p.groups, hi = item_steps(a.c.ix.capacity, a.T, a.k_new != nullptr);
+    if (items < p.groups) hi = min(hi, (w.total + p.groups - items - 1) / (p.groups - items));
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (scan_sum(w.scan, a, [&](int x) { return (x + mid - 1) / mid; }) * a.c.ix.Hkv <= p.groups) hi = mid;
+      if (scan_sum(w.scan, a, [&](int x) { return static_cast<int>(static_cast<unsigned>(x + mid - 1) / static_cast<unsigned>(mid)); }) * a.c.ix.Hkv <= p.groups) hi = mid;
       else lo = mid + 1;
     }
-    const auto pieces = [&](int x) { return (x + lo - 1) / lo; };
+    const auto pieces = [&](int x) { return static_cast<int>(static_cast<unsigned>(x + lo - 1) / static_cast<unsigned>(lo)); };
     if (group >= scan_sum(w.scan, a, pieces) * a.c.ix.Hkv) return;
     w.row = scan_find(w.scan, a, group, pieces);
     w.parts = pieces(w.row.steps);
-    w.place = group - static_cast<int>(w.row.start);
+    w.place = group - w.row.start;
     return;
   }
   w.at = walk_cut(w, p, group);
@@ -296,14 +295,13 @@ __device__ __forceinline__ bool walk_next(Walk& w, const TreeParams& p, int grou
     w.parts = 0;
   } else {
     if (w.at >= w.end) return false;
-    if (w.at >= w.row.start + static_cast<long long>(w.row.steps) * p.a.c.ix.Hkv) scan_next(w.scan, p.a, w.row);
-    const long long in_row = w.at - w.row.start;
-    pc.hk = static_cast<int>(in_row / w.row.steps);
-    pc.j0 = static_cast<int>(in_row - static_cast<long long>(pc.hk) * w.row.steps);
-    const long long left = w.end - w.at;
-    pc.n = w.row.steps - pc.j0 < left ? w.row.steps - pc.j0 : static_cast<int>(left);
+    if (w.at >= w.row.start + w.row.steps * p.a.c.ix.Hkv) scan_next(w.scan, p.a, w.row);
+    const int in_row = w.at - w.row.start;
+    pc.hk = in_row / w.row.steps;
+    pc.j0 = in_row - pc.hk * w.row.steps;
+    pc.n = min(w.row.steps - pc.j0, w.end - w.at);
     if (pc.n < w.row.steps) {
-      const long long i0 = w.at - pc.j0;
+      const int i0 = w.at - pc.j0;
       const InnerCuts c = inner_cuts(w.total, p.groups, i0, i0 + w.row.steps);
       pc.pieces = c.count + 1;
       pc.slot0 = slot_from_begin(c.first);
