@@ -156,6 +156,23 @@ def test_weights_softcap_and_many_heads(ta):
     check_weights(ta, c, p, lse, w)
 
 
+@pytest.mark.parametrize("Hq,Hkv,lens,T", [(8, 1, [700], 700), (8, 1, [1500], 1100), (4, 2, [300, 260], 257), (16, 4, [600], 550)])
+def test_weights_of_a_prompt_shared_by_clusters(ta, Hq, Hkv, lens, T):
+    """Few heads: 2 to 8 CTAs share a unit's queries; several units to a cluster, and CTAs without a query."""
+    c, p, lse, w = weights_case(T, lens, None, T, Hq, Hkv, 64, 64, False)
+    check_weights(ta, c, p, lse, w)
+    outs = []
+    for _ in range(3):
+        out = torch.zeros(c.B, Hkv, c.cap, device="cuda")
+        ta.attn_cache_weights(c.q_t, torch.from_numpy(lse).cuda(), c.cache, None, out, scale=c.scale)
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    counts = [max(1, T // 5)] * len(lens)
+    c, p, lse, w = weights_case(T + 1, lens, counts, T, Hq, Hkv, 64, 128, True)
+    check_weights(ta, c, p, lse, w)
+    assert ta.attn_get_status() == 0
+
+
 def test_weights_of_many_rows(ta):
     lens = [0, 1, 15, 16, 17, 127, 128, 129, 256, 257] * 4
     counts = [min(n, 2) for n in lens]

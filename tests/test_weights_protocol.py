@@ -2,10 +2,11 @@
 interleavings of its warp roles (CPU only).
 
 Roles as in ``tiled_attention_25_b200/csrc/weights_sm100.cu``: the TMA warp
-publishes units and loads K pairs and Q tiles; the column warps fill in each Q
+publishes units and loads their one or two K tiles and the Q tiles; the column warps fill in each Q
 slot's LSE and limits (one arrival here); the MMA warp forms the scores of one
-or two key tiles per Q tile into two buffers each; two warpgroups sum them.  A
-Q tile may stay for the next unit, and a unit may have no queries.
+or two key tiles per Q tile into two buffers each; a warpgroup to each buffer sums
+them, and the two of a tile join their sums.  A Q tile may stay for the next
+unit, and a unit may have no queries.
 
 Checks: no deadlock, no aliasing, and with any one wait of any role running
 out, every role ends with no copy or product in flight.
@@ -15,12 +16,17 @@ import pytest
 from protocol_sim import Sim
 
 
+COLS = 4  # slots of the columns' ring
+
+
 def roles(sim, units, kbufs, qslots, gathered=False):
     """units: (Q tiles, key tiles, new_q, keep_q)."""
     full, empty, drain = sim.full, sim.empty, sim.drain
     for i in range(2):
         sim.bar(f"unit_full{i}", 1)
-        sim.bar(f"unit_empty{i}", 4)
+        sim.bar(f"unit_empty{i}", 6)
+        sim.bar(f"j_full{i}", 1)
+        sim.bar(f"j_empty{i}", 1)
         for t in range(2):
             sim.bar(f"s_full{t}{i}", 1)
             sim.bar(f"s_empty{t}{i}", 1)
@@ -29,8 +35,10 @@ def roles(sim, units, kbufs, qslots, gathered=False):
         sim.bar(f"k_empty{i}", 1)
     for i in range(qslots):
         sim.bar(f"q_full{i}", 1)
+        sim.bar(f"q_empty{i}", 1)
+    for i in range(COLS):
         sim.bar(f"c_full{i}", 1)
-        sim.bar(f"q_empty{i}", 3)
+        sim.bar(f"c_empty{i}", 4)
     sim.bar("drain", 1)
     walk = list(units) + [None]
 
@@ -45,8 +53,8 @@ def roles(sim, units, kbufs, qslots, gathered=False):
                 sim.arrive(f"unit_full{it & 1}")
                 if u is None:
                     return
-                n, _, new, _ = u
-                if n:
+                n, tiles, new, _ = u
+                for _ in range(tiles if n else 0):
                     if not (yield empty(f"k_empty{kn % kbufs}", kn // kbufs)):
                         return
                     sim.load(f"k_full{kn % kbufs}")
@@ -73,9 +81,11 @@ def roles(sim, units, kbufs, qslots, gathered=False):
             if u is None:
                 return
             for _ in range(0 if u[2] else 1, u[0]):
-                if not (yield empty(f"q_empty{ql % qslots}", ql // qslots)):
+                if not (yield empty(f"c_empty{ql % COLS}", ql // COLS)):
                     return
-                sim.arrive(f"c_full{ql % qslots}")
+                if gathered and not (yield empty(f"q_empty{ql % qslots}", ql // qslots)):
+                    return
+                sim.arrive(f"c_full{ql % COLS}")
                 ql += 1
 
     def mma():
@@ -90,29 +100,30 @@ def roles(sim, units, kbufs, qslots, gathered=False):
                 n, tiles, new, keep = u
                 if n == 0:
                     continue
-                if not (yield full(f"k_full{kn % kbufs}", kn // kbufs)):
-                    return
                 for j in range(n):
                     ql += j > 0 or new
-                    if not (yield full(f"c_full{(ql - 1) % qslots}", (ql - 1) // qslots)):
-                        return
-                    if not gathered and not (yield full(f"q_full{(ql - 1) % qslots}", (ql - 1) // qslots)):
+                    ring, of = ("c_full", COLS) if gathered else ("q_full", qslots)
+                    if not (yield full(f"{ring}{(ql - 1) % of}", (ql - 1) // of)):
                         return
                     for t in range(tiles):
+                        k = kn + t
+                        if j == 0 and not (yield full(f"k_full{k % kbufs}", k // kbufs)):
+                            return
                         if not (yield empty(f"s_empty{t}{sc[t] & 1}", sc[t] >> 1)):
                             return
                         sim.commit(f"s_full{t}{sc[t] & 1}")
                         sc[t] += 1
+                        if j == n - 1:
+                            sim.commit(f"k_empty{k % kbufs}")
                     if j < n - 1 or not keep:
                         sim.commit(f"q_empty{(ql - 1) % qslots}")
-                sim.commit(f"k_empty{kn % kbufs}")
-                kn += 1
+                kn += tiles
         yield from body()
         sim.commit("drain")
         yield drain("drain", 0)
 
-    def sums(t):
-        ql = sc = 0
+    def sums(t, sb):
+        ql = sc = joins = 0
         for it, u in enumerate(walk):
             if not (yield full(f"unit_full{it & 1}", it >> 1)):
                 return
@@ -120,19 +131,32 @@ def roles(sim, units, kbufs, qslots, gathered=False):
             if u is None:
                 return
             n, tiles, new, keep = u
+            owner = (sc + max(n, 1) - 1) % 2 == sb
             for j in range(n):
                 ql += j > 0 or new
-                if not (yield full(f"c_full{(ql - 1) % qslots}", (ql - 1) // qslots)):
+                if not (yield full(f"c_full{(ql - 1) % COLS}", (ql - 1) // COLS)):
                     return
                 if t < tiles:
-                    if not (yield full(f"s_full{t}{sc & 1}", sc >> 1)):
-                        return
-                    sim.arrive(f"s_empty{t}{sc & 1}")
+                    if sc % 2 == sb:
+                        if not (yield full(f"s_full{t}{sb}", sc >> 1)):
+                            return
+                        sim.arrive(f"s_empty{t}{sb}")
                     sc += 1
                 if j < n - 1 or not keep:
-                    sim.arrive(f"q_empty{(ql - 1) % qslots}")
+                    sim.arrive(f"c_empty{(ql - 1) % COLS}")
+            if t < tiles and n > 1:
+                if not owner:
+                    if joins and not (yield full(f"j_empty{t}", joins - 1)):
+                        return
+                    sim.arrive(f"j_full{t}")
+                else:
+                    if not (yield full(f"j_full{t}", joins)):
+                        return
+                    sim.arrive(f"j_empty{t}")
+                joins += 1
 
-    return {"tma": tma(), "columns": columns(), "mma": mma(), "sums0": sums(0), "sums1": sums(1)}
+    return {"tma": tma(), "columns": columns(), "mma": mma(),
+            **{f"sums{t}{sb}": sums(t, sb) for t in range(2) for sb in range(2)}}
 
 
 UNITS = {
@@ -145,7 +169,7 @@ UNITS = {
 
 
 @pytest.mark.parametrize("gathered", [False, True])
-@pytest.mark.parametrize("bufs", [(2, 2), (4, 4)])
+@pytest.mark.parametrize("bufs", [(4, 2), (5, 1), (8, 4)])
 @pytest.mark.parametrize("name", sorted(UNITS))
 def test_weights_protocol_never_deadlocks_or_aliases(name, bufs, gathered):
     for seed in range(120):
@@ -155,12 +179,12 @@ def test_weights_protocol_never_deadlocks_or_aliases(name, bufs, gathered):
         assert sim.in_flight_at_exit == 0
 
 
-@pytest.mark.parametrize("role", ["tma", "columns", "mma", "sums0", "sums1"])
+@pytest.mark.parametrize("role", ["tma", "columns", "mma", "sums00", "sums01", "sums11"])
 def test_a_wait_that_runs_out_ends_every_role(role):
     for name in ("prompt", "draft", "half"):
         for at in range(20):
             for seed in range(8):
                 sim = Sim(seed)
-                stuck = sim.run(roles(sim, UNITS[name], 2, 2), give_up=(role, at))
+                stuck = sim.run(roles(sim, UNITS[name], 4, 2), give_up=(role, at))
                 assert stuck is None, f"{role} wait {at}, seed {seed}: {stuck}"
                 assert sim.in_flight_at_exit == 0, f"{role} wait {at}, seed {seed}: {sim.pending_at_exit}"

@@ -11,19 +11,25 @@
 // 128 columns are summed from zero and added to a compensated (Kahan) total:
 // a prompt adds up to a million exponentials into one fp32 number.
 //
-// Bounds.  A draft's few rows: the bytes of K, streamed once (two units' 128
-// KB of K in flight per SM).  A prompt: the exponentials, one per visible
-// (query, key) pair; the products take a quarter of their time.
+// Bounds.  A draft's few rows: the bytes of K, streamed once.  A prompt: the
+// exponentials, one per visible (query, key) pair; the products take a quarter
+// of the time that the special-function unit alone would need, so 3 of 8 pairs
+// of exponentials are evaluated on the FMA pipe (degree 5, 2e-7 relative).
 //
 // Which unit a CTA takes: with one Q tile to a row, an equal contiguous range
 // of the units in (row, head, pair) order, Q staying in shared memory while
 // the head stays; with more, units in the order of their pair index over all
 // rows and heads, i.e. longest first under the causal limit, in a snake.
+// Prompts with fewer units than half the SMs are shared by clusters of 2 to 8
+// CTAs, each of which takes every C-th Q tile of a unit; the sums meet in the
+// first CTA's shared memory and are added in the order of the CTAs.
 //
-// Warp roles (384 threads): warps 0-3 and 4-7 exponentials and sums of key
-// tile 0 and 1 of the pair; warp 8 MMA issuer; warp 9 TMA producer, which
-// publishes the units; warps 10-11 the columns' LSE and limits, and, when a
-// path chooses the queries, the gather of their Q rows.
+// Warp roles (640 threads): four warpgroups of exponentials and sums, two to
+// each key tile of the pair, which take its score buffers in turn (with one to a
+// tile, two warps to an SM quarter, the quarter issued 0.47 instructions a
+// clock: their latencies showed); warp 16 MMA issuer; warp 17 TMA producer,
+// which publishes the units; warps 18-19 the columns' LSE and limits, and, when
+// a path chooses the queries, the gather of their Q rows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,6 +38,7 @@
 #include <cstdint>
 
 #include "cache.h"
+#include "exp2_poly5.h"
 #include "kernel_common.cuh"
 #include "launch.h"
 
@@ -39,52 +46,125 @@ namespace attn25 {
 
 namespace {
 
-constexpr int kWThreads = 384;
+constexpr int kSumWarps = 16, kMmaWarp = 16, kTmaWarp = 17, kColumnWarp = 18;  // and 19
+constexpr int kWThreads = 640;
 constexpr int kMetaThreads = 64;
+constexpr int kColSlots = 4;
 
+constexpr int kMaxSplit = 8;  // CTAs of a cluster
+constexpr int kXStride = (kMaxSplit + 1) * TILE;  // sums of a key tile: the other warpgroup's, the other CTAs'
+
+// Shared memory: Q slots, K slots of one tile each, sums on their way.  With
+// one Q tile to a row (which stays while the head stays) one Q slot and all the
+// rest for K; with more, Q tiles stream as well.
 template <int D>
 struct WCfg {
   static constexpr int kTileBytes = TILE * D * 2;
-  static constexpr int kKBufs = D == 128 ? 2 : 4;  // K pairs in flight: 128 KB
-  static constexpr int kQSlots = D == 128 ? 2 : 4;
-  static constexpr int kQOff = 0;
-  static constexpr int kKOff = kQSlots * kTileBytes;
-  static constexpr int kBarOff = kKOff + kKBufs * 2 * kTileBytes;
-  static constexpr int kSmemBytes = kBarOff + 8192;
+  static constexpr int kTiles = D == 128 ? 6 : 12;  // 192 KB
+  static constexpr int kQSlots = D == 128 ? 2 : 4;  // where Q tiles stream
+  static constexpr int kXOff = kTiles * kTileBytes;
+  static constexpr int kBarOff = kXOff + 2 * (kMaxSplit + 1) * TILE * 4;
+  static constexpr int kSmemBytes = kBarOff + 6144;
   static constexpr int kAllocBytes = kSmemBytes + 1024;
 };
 
 struct Unit {
   int32_t b, hk, kp;     // row, KV head, pair of key tiles; b < 0: the end
   int32_t len, n;        // filled slots and queries of the row
-  int32_t rt0, n_rt;     // Q tiles [rt0, rt0 + n_rt) see some of its keys
+  int32_t rt0, n_rt;     // Q tiles rt0, rt0 + split, ... (n_rt of them) are this CTA's that see some of its keys
   int32_t new_q, keep_q; // the first Q tile has to be loaded / the last one serves the next unit too
 };
 
 struct WBarriers {
   uint64_t unit_full[2], unit_empty[2];
-  uint64_t k_full[4], k_empty[4];
-  uint64_t q_full[4], c_full[4], q_empty[4];  // a Q slot's copies; its columns' values (and gathered rows); both used up
+  uint64_t k_full[12], k_empty[12];
+  uint64_t q_full[4], q_empty[4];  // a Q slot's copies; its products are done
+  // a Q tile's columns (and, with a path, its gathered rows); read.  A ring of its
+  // own, since the sums keep them for longer than the products keep Q.
+  uint64_t c_full[kColSlots], c_empty[kColSlots];
   uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t j_full[2], j_empty[2];  // the other warpgroup's sum of a key tile: written; read
+  uint64_t x_full[2], x_empty[2];  // a cluster's sums: written by the others (first CTA); read (the others)
   uint64_t drain;
   uint32_t tmem_base, abort_flag, never_set;
   Unit unit[2];
-  int32_t min_lim[4][2];           // smallest limit of each half of a Q tile's columns
-  alignas(16) float neg[4][TILE];  // -LSE log2 e of the columns of a Q slot
-  alignas(16) int32_t lim[4][TILE];  // the slots below the column's limit are the ones it sees
+  int32_t min_lim[kColSlots][2];   // smallest limit of each half of a Q tile's columns
+  alignas(16) float neg[kColSlots][TILE];  // -LSE log2 e of the columns
+  alignas(16) int32_t lim[kColSlots][TILE];  // the slots below the column's limit are the ones it sees
 };
-static_assert(sizeof(WBarriers) <= 8192, "barrier block");
+static_assert(sizeof(WBarriers) <= 6144, "barrier block");
 
-constexpr int kUnitReaders = 11;  // MMA warp, 8 sum warps, 2 column warps
+constexpr int kUnitReaders = kSumWarps + 3;  // and the MMA and column warps
 
 struct WParams {
   WeightsArgs a;
   RowTiles rt;
   bool one_tile;  // every row's queries fit one Q tile
+  int split;      // CTAs of a cluster that share a unit
+  int q_slots, k_slots;
+  uint32_t head_magic;  // row / head_tile = row * head_magic >> 16 (rows below 128)
   uint64_t wait_ns;
 };
 
 __device__ __forceinline__ void flag_index(int* status) { atomicCAS(status, 0, kErrIndex); }
+
+// A place in a ring of `n` slots.
+struct SlotPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ bool w_wait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  return mbar_wait_warp_ool(bar, parity, w);
+}
+
+// ------------------------------------------------------------------ cluster
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The bounded warp wait for arrivals of other CTAs (acquire at cluster scope).
+static __device__ __noinline__ bool wait_cluster(uint32_t bar, uint32_t parity, WaitCtl w) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
+    bool give_up = aborted(w);
+    if (!give_up && globaltimer() - t0 > w.limit_ns) {
+      give_up = true;
+      record_error(kErrTimeout, w);
+    }
+    if (__any_sync(0xffffffffu, give_up)) return false;
+  }
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // ------------------------------------------------------------------ units
 //
@@ -160,11 +240,11 @@ __device__ __forceinline__ Unit find_row(WScan& s, const WeightsArgs& a, long lo
 
 // The Q tiles that see some key of the unit: those from the first query at or
 // behind the pair's first slot.
-__device__ __forceinline__ void set_tiles(Unit& u, const RowTiles& rt) {
+__device__ __forceinline__ void set_tiles(Unit& u, const RowTiles& rt, int rank, int split) {
   const int first = u.kp * 2 * TILE - (u.len - u.n);
-  u.rt0 = first > 0 ? first / rt.tok_tile * rt.head_chunks : 0;
+  u.rt0 = (first > 0 ? first / rt.tok_tile * rt.head_chunks : 0) + rank;
   const int all = (u.n + rt.tok_tile - 1) / rt.tok_tile * rt.head_chunks;
-  u.n_rt = all > u.rt0 ? all - u.rt0 : 0;
+  u.n_rt = all > u.rt0 ? (all - u.rt0 + split - 1) / split : 0;
   u.new_q = u.n_rt > 0;
   u.keep_q = 0;
 }
@@ -184,6 +264,24 @@ __device__ __forceinline__ QTile q_tile(const RowTiles& rt, int G, int n, int ti
 
 // ------------------------------------------------------------------ sums
 //
+// 2^x of a pair on the FMA pipe (the forward kernel's range reduction, degree
+// 5).  x is at most about 0 where the LSE belongs to the scores; the clamps keep
+// other values from wrapping the exponent (2^128 and more come out as 2^127.99).
+__device__ __forceinline__ float2 exp2_poly5(float2 x) {
+  x.x = fminf(fmaxf(x.x, -126.f), 127.99f);
+  x.y = fminf(fmaxf(x.y, -126.f), 127.99f);
+  const float2 t = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
+  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+  float2 p = __ffma2_rn(make_float2(kExp2E5, kExp2E5), f, make_float2(kExp2E4, kExp2E4));
+  p = __ffma2_rn(p, f, make_float2(kExp2E3, kExp2E3));
+  p = __ffma2_rn(p, f, make_float2(kExp2E2, kExp2E2));
+  p = __ffma2_rn(p, f, make_float2(kExp2E1, kExp2E1));
+  p = __ffma2_rn(p, f, make_float2(kExp2E0, kExp2E0));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
 // One thread's 32 columns: 2^(x sl2 + neg), added into acc (pairs).
 template <bool SOFTCAP>
 __device__ __forceinline__ void sum_full(const uint32_t (&x)[32], const float* neg, float sl2, float cap_in, float cap_out,
@@ -202,8 +300,10 @@ __device__ __forceinline__ void sum_full(const uint32_t (&x)[32], const float* n
       a0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(ng.x, ng.y));
       a1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(ng.z, ng.w));
     }
+    // pairs 1 and 5 of every 8 on the FMA pipe
+    const int pair = e / 2 % 8;
     acc[0] = __fadd2_rn(acc[0], make_float2(ex2_approx(a0.x), ex2_approx(a0.y)));
-    acc[1] = __fadd2_rn(acc[1], make_float2(ex2_approx(a1.x), ex2_approx(a1.y)));
+    acc[1] = __fadd2_rn(acc[1], pair == 0 || pair == 4 ? exp2_poly5(a1) : make_float2(ex2_approx(a1.x), ex2_approx(a1.y)));
   }
 }
 
@@ -231,23 +331,35 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   WBarriers* bars = reinterpret_cast<WBarriers*>(smem + Cfg::kBarOff);
   const uint32_t sbase = smem_u32(smem);
+  const uint32_t k_ring = sbase + p.q_slots * Cfg::kTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? static_cast<int>(cta_rank()) : 0;
+  const int walkers = gridDim.x / p.split, walker = blockIdx.x / p.split;  // clusters walk together
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->unit_full[i]), 1);
       mbar_init(smem_u32(&bars->unit_empty[i]), kUnitReaders);
+      mbar_init(smem_u32(&bars->j_full[i]), 4);
+      mbar_init(smem_u32(&bars->j_empty[i]), 4);
+      mbar_init(smem_u32(&bars->x_full[i]), max(1, (p.split - 1) * TILE));  // (unused where split is 1)
+      mbar_init(smem_u32(&bars->x_empty[i]), 4);
       for (int t = 0; t < 2; ++t) {
         mbar_init(smem_u32(&bars->s_full[t][i]), 1);
         mbar_init(smem_u32(&bars->s_empty[t][i]), 4);
       }
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 12; ++i) {
       mbar_init(smem_u32(&bars->k_full[i]), 1);
       mbar_init(smem_u32(&bars->k_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
+      mbar_init(smem_u32(&bars->q_empty[i]), 1);
+    }
+    for (int i = 0; i < kColSlots; ++i) {
       mbar_init(smem_u32(&bars->c_full[i]), kMetaThreads);
-      mbar_init(smem_u32(&bars->q_empty[i]), 1 + 8);
+      mbar_init(smem_u32(&bars->c_empty[i]), kSumWarps);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
@@ -255,36 +367,37 @@ __global__ void __launch_bounds__(kWThreads, 1)
     fence_mbar_init();
   }
   // rows that no Q tile fills stay zero (their columns' sums then add 2^-inf)
-  for (int s = 0; s < Cfg::kQSlots; ++s)
+  for (int s = 0; s < p.q_slots; ++s)
     for (int i = threadIdx.x; i < (TILE - p.rt.rows) * (D / 8); i += kWThreads) {
       const int row = p.rt.rows + i / (D / 8), ch = i % (D / 8);
-      *reinterpret_cast<uint4*>(smem + Cfg::kQOff + s * Cfg::kTileBytes + (ch >> 3) * (TILE * 128) + row * 128 + (ch & 7) * 16) =
+      *reinterpret_cast<uint4*>(smem + s * Cfg::kTileBytes + (ch >> 3) * (TILE * 128) + row * 128 + (ch & 7) * 16) =
           make_uint4(0u, 0u, 0u, 0u);
     }
   fence_proxy_async_smem();
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
   }
   tc_fence_before();
   __syncthreads();
+  if (p.split > 1) cluster_sync_all();  // the others' barriers are there
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{p.wait_ns, smem_u32(&bars->abort_flag), a.c.status};
 
-  if (warp == 9) {
+  if (warp == kTmaWarp) {
     // ------------------------------------------------------------ TMA producer
     const int ps = a.c.ix.page_size;
     const int box_rows = ps < TILE ? ps : TILE;
     WScan scan;
     w_load(scan, a, 0);
     const long long total = units_below(scan, a, INT_MAX);
-    long long at = raw_cut(total, gridDim.x, blockIdx.x);
-    const long long end = raw_cut(total, gridDim.x, blockIdx.x + 1);
+    long long at = raw_cut(total, walkers, walker);
+    const long long end = raw_cut(total, walkers, walker + 1);
     auto nth = [&](long long u) {  // unit u in the order of the grid's walk
       Unit x;
       if (p.one_tile) {
@@ -305,7 +418,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         x.hk = static_cast<int>(u);
         x.kp = lo;
       }
-      set_tiles(x, p.rt);
+      set_tiles(x, p.rt, rank, p.split);
       return x;
     };
     Unit next{};
@@ -313,10 +426,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     int wave = 0;
     if (p.one_tile) {
       if (at < end) next = nth(at);
-    } else if (blockIdx.x < total) {
-      next = nth(blockIdx.x);
+    } else if (walker < total) {
+      next = nth(walker);
     }
-    uint32_t kn = 0, ql = 0;
+    SlotPos kp, qp;
+    uint32_t k_copies = 0, q_copies = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       Unit u = next;
@@ -337,13 +451,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
           }
         } else {
           ++wave;
-          const long long base = static_cast<long long>(wave) * gridDim.x;
-          const long long v = (wave & 1) ? base + gridDim.x - 1 - blockIdx.x : base + blockIdx.x;
+          const long long base = static_cast<long long>(wave) * walkers;
+          const long long v = (wave & 1) ? base + walkers - 1 - walker : base + walker;
           if (v < total) next = nth(v);
         }
       }
       const int buf = it & 1;
-      if (!mbar_wait_warp(smem_u32(&bars->unit_empty[buf]), ((it >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+      if (!w_wait(smem_u32(&bars->unit_empty[buf]), ((it >> 1) & 1) ^ 1, wc)) { ok = false; break; }
       if (lane == 0) {
         bars->unit[buf] = u;
         mbar_arrive(smem_u32(&bars->unit_full[buf]));
@@ -351,110 +465,133 @@ __global__ void __launch_bounds__(kWThreads, 1)
       __syncwarp();
       if (u.b < 0) break;
       if (u.n_rt > 0) {
-        // K of both tiles: the pages that hold filled slots, one box of a page
-        // and 64 columns to a lane (at most 16 pages x 2)
+        // K of one or two tiles: the pages that hold filled slots, looked up for both at once
         const int s0 = u.kp * 2 * TILE, used = min(2 * TILE, u.len - s0), boxes = (used + box_rows - 1) / box_rows;
-        const int bx = lane / (D / 64), c = lane % (D / 64), kb = kn % Cfg::kKBufs;
-        int page = a.c.ix.num_pages;  // past the pool: the copy fills in zeros
-        const bool mine = bx < boxes;
-        if (mine) {
-          const int e = page_at(a.c.ix, u.b, (s0 + bx * box_rows) / ps);
-          if (e >= 0) page = e;
-          else flag_index(a.c.status);
+        const int per_tile = TILE / box_rows;
+        int entry = 0;  // of page `lane` of the pair
+        if (lane < boxes) {
+          const long long e = static_cast<long long>(u.b) * a.c.ix.max_pages + (s0 + lane * box_rows) / ps;
+          entry = a.c.ix.table != nullptr ? __ldg(a.c.ix.table + e) : static_cast<int>(e);
         }
-        if (!mbar_wait_warp(smem_u32(&bars->k_empty[kb]), ((kn / Cfg::kKBufs) & 1) ^ 1, wc)) { ok = false; break; }
-        const uint32_t bar = smem_u32(&bars->k_full[kb]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
-        __syncwarp();
-        const int row = bx * box_rows;  // within the pair
-        if (mine)
-          tma_load_4d(sbase + Cfg::kKOff + (kb * 2 + row / TILE) * Cfg::kTileBytes + c * (TILE * 128) + row % TILE * 128, &tm_k,
-                      bar, c * 64, ps > TILE ? (s0 + row) % ps : 0, u.hk, page);
-        __syncwarp();
-        ++kn;
+        const int y0 = ps > TILE ? s0 % ps : 0;  // (a pair may end in the next page)
+        for (int t = 0; t < 2 && t * TILE < used; ++t) {
+          if (!w_wait(smem_u32(&bars->k_empty[kp.slot]), kp.phase ^ 1, wc)) { ok = false; break; }
+          const uint32_t bar = smem_u32(&bars->k_full[kp.slot]), dst = k_ring + kp.slot * Cfg::kTileBytes;
+          const int end = min(boxes, (t + 1) * per_tile);
+          if (lane == 0) mbar_arrive_expect_tx(bar, (end - t * per_tile) * box_rows * D * 2);
+          for (int i = t * per_tile; i < end; ++i) {
+            int page = __shfl_sync(0xffffffffu, entry, i);
+            const bool outside = page < 0 || page >= a.c.ix.num_pages;
+            if (outside) page = a.c.ix.num_pages;  // past the pool: the copy fills in zeros
+            if (lane == 0) {
+              if (outside) flag_index(a.c.status);
+              const int y = ps > TILE ? (y0 + t * TILE) % ps : 0;
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(dst + c * (TILE * 128) + (i - t * per_tile) * box_rows * 128, &tm_k, bar, c * 64, y, u.hk, page);
+            }
+          }
+          __syncwarp();
+          kp.next(p.k_slots);
+          ++k_copies;
+        }
+        if (!ok) break;
       }
       // Q tiles (with a path the column warps gather them instead)
       for (int j = u.new_q ? 0 : 1; a.path == nullptr && j < u.n_rt; ++j) {
-        const int slot = ql % Cfg::kQSlots;
-        if (!mbar_wait_warp(smem_u32(&bars->q_empty[slot]), ((ql / Cfg::kQSlots) & 1) ^ 1, wc)) { ok = false; break; }
+        if (!w_wait(smem_u32(&bars->q_empty[qp.slot]), qp.phase ^ 1, wc)) { ok = false; break; }
         if (lane == 0) {
-          const uint32_t bar = smem_u32(&bars->q_full[slot]);
-          const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j);
+          const uint32_t bar = smem_u32(&bars->q_full[qp.slot]);
+          const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
           mbar_arrive_expect_tx(bar, p.rt.rows * D * 2);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sbase + Cfg::kQOff + slot * Cfg::kTileBytes + c * (TILE * 128), &tm_q, bar, c * 64,
-                        u.hk * a.G + q.h0, q.i0, u.b);
+            tma_load_4d(sbase + qp.slot * Cfg::kTileBytes + c * (TILE * 128), &tm_q, bar, c * 64, u.hk * a.G + q.h0, q.i0, u.b);
         }
         __syncwarp();
-        ++ql;
+        qp.next(p.q_slots);
+        ++q_copies;
       }
     }
     if (lane == 0) {  // let the copies in flight land before the CTA exits
       const WaitCtl drain_wc{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status};
-      for (uint32_t s = 0; s < Cfg::kKBufs; ++s) {
-        const uint32_t uses = (kn + Cfg::kKBufs - 1 - s) / Cfg::kKBufs;
+      for (int s = 0; s < p.k_slots; ++s) {
+        const int uses = (static_cast<int>(k_copies) + p.k_slots - 1 - s) / p.k_slots;
         if (uses > 0) mbar_wait_thread(smem_u32(&bars->k_full[s]), (uses - 1) & 1, drain_wc);
       }
-      for (uint32_t s = 0; s < Cfg::kQSlots; ++s) {
-        const uint32_t uses = (ql + Cfg::kQSlots - 1 - s) / Cfg::kQSlots;
+      for (int s = 0; s < p.q_slots; ++s) {
+        const int uses = (static_cast<int>(q_copies) + p.q_slots - 1 - s) / p.q_slots;
         if (uses > 0) mbar_wait_thread(smem_u32(&bars->q_full[s]), (uses - 1) & 1, drain_wc);
       }
     }
-  } else if (warp >= 10) {
+  } else if (warp >= kColumnWarp) {
     // ------------------------------------------------------------ columns of the Q tiles
-    const int m = threadIdx.x - 10 * 32;
-    uint32_t ql = 0;
+    const int m = threadIdx.x - kColumnWarp * 32;
+    SlotPos qp, cp;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int buf = it & 1;
-      if (!mbar_wait_warp(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
       const Unit u = bars->unit[buf];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
       if (u.b < 0) break;
-      for (int j = u.new_q ? 0 : 1; j < u.n_rt; ++j) {
-        const int slot = ql % Cfg::kQSlots;
-        const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j);
-        // read ahead of the slot: its columns' LSE and nodes
-        float neg[2];
-        int lim[2], low = INT_MAX;
-        bool bad = false;
+      // this thread's two columns of tile j: read one tile ahead, looked at when it is published
+      float lse[2] = {};
+      int lim[2] = {};
+      bool real[2] = {};
+      auto fetch = [&](int j) {
+        const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int r = m + 64 * x, i = q.i0 + r / p.rt.head_tile, head = q.h0 + r % p.rt.head_tile;
-          neg[x] = -INFINITY;
-          lim[x] = INT_MAX;
-          if (r < p.rt.rows) {
-            int node = i;
-            if (i < u.n && a.path != nullptr) {
-              node = a.path[static_cast<long long>(u.b) * a.T + i];
-              if (node < 0 || node >= a.T) bad = true;
+          const int r = m + 64 * x, r_tok = static_cast<int>(r * p.head_magic >> 16), i = q.i0 + r_tok;
+          const int head = q.h0 + r - r_tok * p.rt.head_tile;
+          int node = i;
+          real[x] = r < p.rt.rows && i < u.n && head < a.G;
+          if (real[x] && a.path != nullptr) {
+            node = a.path[static_cast<long long>(u.b) * a.T + i];
+            if (node < 0 || node >= a.T) {
+              real[x] = false;
+              flag_index(a.c.status);
             }
-            const bool real = i < u.n && head < a.G && node >= 0 && node < a.T;
-            // a gathered tile holds zeros where there is no query: its column adds 2^-inf
-            const bool zeros = a.path != nullptr && !real;
-            lim[x] = real ? u.len - u.n + i + 1 : (zeros ? INT_MAX : 0);
-            neg[x] = real ? -a.lse[(static_cast<long long>(u.b) * a.Hq + u.hk * a.G + head) * a.T + node] * LOG2E : -INFINITY;
-            if (r < q.cols) low = min(low, lim[x]);
           }
+          // what no query fills holds zeros behind the tile's rows and where rows are
+          // gathered: its column adds 2^-inf; elsewhere it may hold anything and is left out
+          const bool zeros = r >= p.rt.rows || a.path != nullptr;
+          lim[x] = real[x] ? u.len - u.n + i + 1 : (zeros ? INT_MAX : 0);
+          if (real[x]) lse[x] = __ldg(a.lse + (static_cast<long long>(u.b) * a.Hq + u.hk * a.G + head) * a.T + node);
         }
-        if (bad) flag_index(a.c.status);
+      };
+      const int j0 = u.new_q ? 0 : 1;
+      if (j0 < u.n_rt) fetch(j0);
+#pragma unroll 1
+      for (int j = j0; j < u.n_rt; ++j) {
+        const int slot = cp.slot;
+        const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
+        const float lse_now[2] = {lse[0], lse[1]};
+        const int lim_now[2] = {lim[0], lim[1]};
+        const bool real_now[2] = {real[0], real[1]};
+        if (j + 1 < u.n_rt) fetch(j + 1);
+        int low = INT_MAX;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
-        if (!mbar_wait_warp(smem_u32(&bars->q_empty[slot]), ((ql / Cfg::kQSlots) & 1) ^ 1, wc)) { ok = false; break; }
-        if (lane == 0) bars->min_lim[slot][warp - 10] = low;
+        for (int x = 0; x < 2; ++x)
+          if (m + 64 * x < q.cols) low = min(low, lim_now[x]);
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (!w_wait(smem_u32(&bars->c_empty[slot]), cp.phase ^ 1, wc)) { ok = false; break; }
+        if (lane == 0) bars->min_lim[slot][warp - kColumnWarp] = low;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          bars->neg[slot][m + 64 * x] = neg[x];
-          bars->lim[slot][m + 64 * x] = lim[x];
+          bars->neg[slot][m + 64 * x] = real_now[x] ? -lse_now[x] * LOG2E : -INFINITY;
+          bars->lim[slot][m + 64 * x] = lim_now[x];
         }
         if (a.path != nullptr) {
           // the chosen queries' rows, in the 128-byte swizzle: chunk c of row r at c ^ (r & 7)
-          uint8_t* dst = smem + Cfg::kQOff + slot * Cfg::kTileBytes;
+          if (!w_wait(smem_u32(&bars->q_empty[qp.slot]), qp.phase ^ 1, wc)) { ok = false; break; }
+          uint8_t* dst = smem + qp.slot * Cfg::kTileBytes;
 #pragma unroll 4
           for (int x = m; x < q.cols * (D / 8); x += kMetaThreads) {
-            const int r = x / (D / 8), ch = x % (D / 8), i = q.i0 + r / p.rt.head_tile, head = q.h0 + r % p.rt.head_tile;
+            const int r = x / (D / 8), ch = x % (D / 8), r_tok = static_cast<int>(r * p.head_magic >> 16), i = q.i0 + r_tok,
+                      head = q.h0 + r - r_tok * p.rt.head_tile;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (r < q.rows && head < a.G) {
               const int node = a.path[static_cast<long long>(u.b) * a.T + i];
@@ -465,45 +602,60 @@ __global__ void __launch_bounds__(kWThreads, 1)
             *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
           }
           fence_proxy_async_smem();
+          qp.next(p.q_slots);
         }
         mbar_arrive(smem_u32(&bars->c_full[slot]));
-        ++ql;
+        cp.next(kColSlots);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    uint32_t kn = 0, ql = 0, sc[2] = {0, 0};
+    SlotPos kp, qp, cp, cur, cols;  // cur, cols: the Q and column slots in use
+    uint32_t sc[2] = {0, 0};
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int buf = it & 1;
-      if (!mbar_wait_warp(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
       const Unit u = bars->unit[buf];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
       if (u.b < 0) break;
       if (u.n_rt == 0) continue;
-      const int kb = kn % Cfg::kKBufs;
-      if (!mbar_wait_warp(smem_u32(&bars->k_full[kb]), (kn / Cfg::kKBufs) & 1, wc)) break;
-      ++kn;
       const int tiles = u.len - u.kp * 2 * TILE > TILE ? 2 : 1;
+      SlotPos kt[2];
+      for (int t = 0; t < tiles; ++t) {
+        kt[t] = kp;
+        kp.next(p.k_slots);
+      }
+#pragma unroll 1
       for (int j = 0; j < u.n_rt && ok; ++j) {
-        if (j > 0 || u.new_q) ++ql;  // load ql - 1 is the one in use
-        const int slot = (ql - 1) % Cfg::kQSlots;
-        const uint32_t phase = ((ql - 1) / Cfg::kQSlots) & 1;
-        if (!mbar_wait_warp(smem_u32(&bars->c_full[slot]), phase, wc) ||
-            (a.path == nullptr && !mbar_wait_warp(smem_u32(&bars->q_full[slot]), phase, wc))) {
+        if (j > 0 || u.new_q) {
+          cur = qp;
+          qp.next(p.q_slots);
+          cols = cp;
+          cp.next(kColSlots);
+        }
+        // (gathered rows come with their columns)
+        if (!(a.path == nullptr ? w_wait(smem_u32(&bars->q_full[cur.slot]), cur.phase, wc)
+                                : w_wait(smem_u32(&bars->c_full[cols.slot]), cols.phase, wc))) {
           ok = false;
           break;
         }
-        const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j);
+        const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
         const uint32_t idesc = idesc_bf16_f32(128, q.cols, false, false);
-        const uint32_t q_smem = sbase + Cfg::kQOff + slot * Cfg::kTileBytes;
+        const uint32_t q_smem = sbase + cur.slot * Cfg::kTileBytes;
+#pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
           const int sb = sc[t] & 1;
-          if (!mbar_wait_warp(smem_u32(&bars->s_empty[t][sb]), ((sc[t] >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+          const SlotPos ks = t == 0 ? kt[0] : kt[1];
+          if ((j == 0 && !w_wait(smem_u32(&bars->k_full[ks.slot]), ks.phase, wc)) ||
+              !w_wait(smem_u32(&bars->s_empty[t][sb]), ((sc[t] >> 1) & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           ++sc[t];
-          const uint32_t k_smem = sbase + Cfg::kKOff + (kb * 2 + t) * Cfg::kTileBytes;
+          const uint32_t k_smem = k_ring + ks.slot * Cfg::kTileBytes;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (TILE * 128) + (kk & 3) * 32;
@@ -511,84 +663,114 @@ __global__ void __launch_bounds__(kWThreads, 1)
                      smem_desc_sw128(q_smem + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
           }
           mma_commit_w(smem_u32(&bars->s_full[t][sb]));
+          if (j == u.n_rt - 1) mma_commit_w(smem_u32(&bars->k_empty[ks.slot]));
         }
-        if (ok && (j < u.n_rt - 1 || !u.keep_q)) mma_commit_w(smem_u32(&bars->q_empty[slot]));
+        if (ok && (j < u.n_rt - 1 || !u.keep_q)) mma_commit_w(smem_u32(&bars->q_empty[cur.slot]));
       }
-      if (ok) mma_commit_w(smem_u32(&bars->k_empty[kb]));
     }
     mma_commit_w(smem_u32(&bars->drain));
-    mbar_wait_warp(smem_u32(&bars->drain), 0, WaitCtl{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status});
+    w_wait(smem_u32(&bars->drain), 0, WaitCtl{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status});
   } else {
     // ------------------------------------------------------------ exponentials and sums
-    const int t = warp >> 2, r = threadIdx.x & 127;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int t = (warp >> 2) & 1, sb = warp >> 3, r = threadIdx.x & 127;  // key tile, score buffer, key
+    const uint32_t s_addr = tmem + (t * 2 + sb) * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const float sl2 = a.scale * LOG2E;
     const float cap_in = SOFTCAP ? a.scale / a.softcap : 0.f, cap_out = SOFTCAP ? a.softcap * LOG2E : 0.f;
-    uint32_t ql = 0, sc = 0;
+    SlotPos cp, cur;
+    uint32_t sc = 0;      // steps of the tile so far: buffer sc & 1 holds the next
+    uint32_t joins = 0, shared = 0;  // units that both warpgroups, or several CTAs, had a part of
+    float* x_buf = reinterpret_cast<float*>(smem + Cfg::kXOff) + t * kXStride;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int buf = it & 1;
-      if (!mbar_wait_warp(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
       const Unit u = bars->unit[buf];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
       if (u.b < 0) break;
       const int key0 = u.kp * 2 * TILE + t * TILE, key = key0 + r;
       const bool here = key0 < u.len;  // the second tile of a row's last pair may hold nothing
+      // the warpgroup that takes the last step writes the unit (without steps: the one whose turn it is)
+      const bool owner = ((sc + (u.n_rt > 0 ? u.n_rt - 1 : 0)) & 1) == static_cast<uint32_t>(sb);
       const long long entry = slot_entry(a.c.ix, u.b, u.hk, key);
       float base = 0.f;
-      if (a.w_in != nullptr && key < u.len - u.n) base = a.w_in[entry];
+      if (owner && rank == 0 && a.w_in != nullptr && key < u.len - u.n) base = a.w_in[entry];
       float total = 0.f, lost = 0.f;
+#pragma unroll 1
       for (int j = 0; j < u.n_rt; ++j) {
-        if (j > 0 || u.new_q) ++ql;
-        const int slot = (ql - 1) % Cfg::kQSlots;
-        // (waited for also where the tile holds nothing, so that no slot is handed back twice in one use)
-        if (!mbar_wait_warp(smem_u32(&bars->c_full[slot]), ((ql - 1) / Cfg::kQSlots) & 1, wc)) { ok = false; break; }
+        if (j > 0 || u.new_q) {
+          cur = cp;
+          cp.next(kColSlots);
+        }
+        const int slot = cur.slot;
+        // (waited for also where there is nothing to do, so that no slot is handed back twice in one use)
+        if (!w_wait(smem_u32(&bars->c_full[slot]), cur.phase, wc)) { ok = false; break; }
         if (here) {
-          const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j);
-          const int sb = sc & 1;
-          if (!mbar_wait_warp(smem_u32(&bars->s_full[t][sb]), (sc >> 1) & 1, wc)) { ok = false; break; }
-          ++sc;
-          tc_fence_after();
-          const uint32_t s_addr = tmem + (t * 2 + sb) * 128 + lane_off;
-          const float* neg = bars->neg[slot];
-          const int32_t* lim = bars->lim[slot];
-          const bool full = min(bars->min_lim[slot][0], bars->min_lim[slot][1]) >= key0 + TILE;
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const int chunks = q.cols / 32;
-          uint32_t x[2][32];
-          tmem_ld32(s_addr, x[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c < chunks) {
+          if ((sc & 1) == static_cast<uint32_t>(sb)) {
+            const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
+            if (!w_wait(smem_u32(&bars->s_full[t][sb]), (sc >> 1) & 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            const bool full = min(bars->min_lim[slot][0], bars->min_lim[slot][1]) >= key0 + TILE;
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+            for (int c = 0; c < q.cols; c += 32) {
+              uint32_t x[32];
+              tmem_ld32(s_addr + c, x);
               tmem_wait_ld();
-              if (c + 1 < chunks) {
-                if (c < 3) tmem_ld32(s_addr + (c + 1) * 32, x[(c + 1) & 1]);
-              } else {  // the scores are read: the buffer is free
+              if (c + 32 >= q.cols) {  // the scores are read
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[t][sb]));
               }
-              if (full) sum_full<SOFTCAP>(x[c & 1], neg + c * 32, sl2, cap_in, cap_out, acc);
-              else sum_limited<SOFTCAP>(x[c & 1], neg + c * 32, lim + c * 32, key, sl2, cap_in, cap_out, acc);
+              if (full) sum_full<SOFTCAP>(x, bars->neg[slot] + c, sl2, cap_in, cap_out, acc);
+              else sum_limited<SOFTCAP>(x, bars->neg[slot] + c, bars->lim[slot] + c, key, sl2, cap_in, cap_out, acc);
             }
+            const float tile_sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            const float y = tile_sum - lost, z = total + y;  // Kahan
+            lost = (z - total) - y;
+            total = z;
           }
-          const float tile_sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-          const float y = tile_sum - lost, z = total + y;  // Kahan
-          lost = (z - total) - y;
-          total = z;
+          ++sc;
         }
         __syncwarp();
-        if (lane == 0 && (j < u.n_rt - 1 || !u.keep_q)) mbar_arrive(smem_u32(&bars->q_empty[slot]));
+        if (lane == 0 && (j < u.n_rt - 1 || !u.keep_q)) mbar_arrive(smem_u32(&bars->c_empty[slot]));
       }
       if (!ok) break;
-      if (key < u.len) a.w_out[entry] = base + total;
+      if (here && u.n_rt > 1) {  // both warpgroups had steps
+        if (!owner) {
+          if (joins > 0 && !w_wait(smem_u32(&bars->j_empty[t]), (joins - 1) & 1, wc)) break;
+          x_buf[r] = total;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->j_full[t]));
+        } else {
+          if (!w_wait(smem_u32(&bars->j_full[t]), joins & 1, wc)) break;
+          total += x_buf[r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->j_empty[t]));
+        }
+        ++joins;
+      }
+      if (p.split > 1) {
+        if (owner && rank > 0) {  // hand the sum to the first CTA once it has read the last unit's
+          if (shared > 0 && !wait_cluster(smem_u32(&bars->x_empty[t]), (shared - 1) & 1, wc)) break;
+          st_cluster(in_cta(smem_u32(x_buf + rank * TILE + r), 0), total);
+          arrive_cluster(in_cta(smem_u32(&bars->x_full[t]), 0));
+        } else if (owner) {
+          if (!wait_cluster(smem_u32(&bars->x_full[t]), shared & 1, wc)) break;
+          for (int x = 1; x < p.split; ++x) total += x_buf[x * TILE + r];
+          __syncwarp();
+          if (lane > 0 && lane < p.split) arrive_cluster(in_cta(smem_u32(&bars->x_empty[t]), lane));
+        }
+        ++shared;
+      }
+      if (owner && rank == 0 && key < u.len) a.w_out[entry] = base + total;
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (p.split > 1) cluster_sync_all();  // no CTA leaves while another may reach into its shared memory
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 template <int D, bool SOFTCAP>
@@ -597,8 +779,18 @@ cudaError_t launch_weights_t(const CUtensorMap& tq, const CUtensorMap& tk, const
   static std::atomic<uint64_t> done{0};
   cudaError_t e = prepare_kernel(done, kernel, WCfg<D>::kAllocBytes, 0);
   if (e != cudaSuccess) return e;
-  kernel<<<sms, kWThreads, WCfg<D>::kAllocBytes, stream>>>(tq, tk, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(sms / p.split * p.split);
+  cfg.blockDim = dim3(kWThreads);
+  cfg.dynamicSmemBytes = WCfg<D>::kAllocBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = p.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tk, p);
 }
 
 }  // namespace
@@ -609,6 +801,16 @@ cudaError_t launch_cache_weights(const CUtensorMap& tq, const CUtensorMap& tk, c
   p.a = a;
   p.rt = row_tiles(a.G, a.T);
   p.one_tile = p.rt.tiles == 1;
+  const int q_slots = a.c.D == 128 ? WCfg<128>::kQSlots : WCfg<64>::kQSlots, tiles = a.c.D == 128 ? WCfg<128>::kTiles : WCfg<64>::kTiles;
+  p.q_slots = p.one_tile ? 1 : q_slots;
+  p.k_slots = tiles - p.q_slots;
+  // a prompt's units (its new tokens alone): shared while they fill less than half the SMs
+  p.split = 1;
+  if (!p.one_tile) {
+    const long long units = static_cast<long long>(a.c.ix.B) * a.c.ix.Hkv * ((a.T + 2 * TILE - 1) / (2 * TILE));
+    while (p.split < kMaxSplit && units * p.split * 2 <= sms && p.rt.tiles >= p.split * 2) p.split *= 2;
+  }
+  p.head_magic = 65535u / p.rt.head_tile + 1;
   p.wait_ns = wait_ns;
   if (a.c.D == 128) return a.softcap > 0.f ? launch_weights_t<128, true>(tq, tk, p, sms, stream) : launch_weights_t<128, false>(tq, tk, p, sms, stream);
   return a.softcap > 0.f ? launch_weights_t<64, true>(tq, tk, p, sms, stream) : launch_weights_t<64, false>(tq, tk, p, sms, stream);
