@@ -1,4 +1,4 @@
-"""Generate exp2_poly.h and exp2_poly5.h: minimax polynomials for 2^f on [-1/2, 1/2].
+"""Generate exp2_poly.h: a minimax polynomial for 2^f on [-1/2, 1/2].
 
 The forward kernel evaluates part of its exponentials on the FMA pipe
 instead of the special-function unit: 2^x = 2^n * 2^f with n = round(x),
@@ -7,17 +7,15 @@ polynomial whose coefficients minimise the maximum RELATIVE error on
 [-1/2, 1/2] (Remez exchange algorithm).  The probabilities are rounded to
 bfloat16 (relative step 2^-8) right after, so degree 3 (relative error below
 8e-5) leaves the polynomial far under that rounding, and each evaluation one
-FMA shorter than degree 4 (below 3e-6).  The slot weights are fp32 sums of
-exponentials, so theirs take degree 5 (below 2e-7, the size of the hardware
-exponential's own error).
+FMA shorter than degree 4 (below 3e-6).
 
-Run:  python tiled_attention_25_b200/csrc/gen_exp2_poly.py  (rewrites both)
+Run:  python tiled_attention_25_b200/csrc/gen_exp2_poly.py  (rewrites exp2_poly.h)
 """
 import os
 
 import numpy as np
 
-HEADERS = ((3, "exp2_poly.h", "C"), (5, "exp2_poly5.h", "E"))  # degree, file, letter of the names
+DEGREE = 3
 LO, HI = -0.5, 0.5
 
 
@@ -51,14 +49,14 @@ def remez_relative(deg, lo, hi, iters=30):
     return c, float(np.max(np.abs(err)))
 
 
-def write(degree, name, letter):
-    c, e = remez_relative(degree, LO, HI)
+def main():
+    c, e = remez_relative(DEGREE, LO, HI)
     c32 = c.astype(np.float32)
     grid = np.linspace(LO, HI, 200001)
     e32 = float(np.max(np.abs((np.polyval(c32.astype(np.float64)[::-1], grid) - np.exp2(grid)) / np.exp2(grid))))
     lines = [
         "// Generated by gen_exp2_poly.py: minimax (relative error) polynomial for 2^f,",
-        f"// f in [{LO}, {HI}], degree {degree}; max relative error {e:.3e} (float64",
+        f"// f in [{LO}, {HI}], degree {DEGREE}; max relative error {e:.3e} (float64",
         f"// coefficients), {e32:.3e} with the float32 coefficients below.",
         "#pragma once",
         "",
@@ -66,17 +64,12 @@ def write(degree, name, letter):
         "",
     ]
     for i, v in enumerate(c32):
-        lines.append(f"constexpr float kExp2{letter}{i} = {float(v)!r}f;")
+        lines.append(f"constexpr float kExp2C{i} = {float(v)!r}f;")
     lines += ["", "}  // namespace attn25", ""]
-    out = os.path.join(os.path.dirname(os.path.abspath(__file__)), name)
+    out = os.path.join(os.path.dirname(os.path.abspath(__file__)), "exp2_poly.h")
     with open(out, "w") as fh:
         fh.write("\n".join(lines))
     print(out, e, e32)
-
-
-def main():
-    for h in HEADERS:
-        write(*h)
 
 
 if __name__ == "__main__":

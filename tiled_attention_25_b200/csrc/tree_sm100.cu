@@ -719,27 +719,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             ++p_cnt[t];
             tc_fence_after();
-            const uint32_t v_smem = v_ring + vp.slot * Cfg::kTileBytes;
+            const uint32_t v_lo = smem_desc_lo(v_ring + vp.slot * Cfg::kTileBytes, TILE * 128);
             const int kks = (max(step_keys(a, pc, pc.j0 + i - 2), 1) + 15) / 16;
 #pragma unroll
             for (int kk = 0; kk < TILE / 16; ++kk)
               if (kk < kks)
-                mma_ts_w(tmem + 256 + t * D, tmem + t * 128 + kk * 8, smem_desc_sw128(v_smem + kk * 2048, TILE * 128, 1024),
-                         Cfg::kIdescPV, (i > 3 || kk > 0) ? 1u : 0u);
+                mma_ts_lo_w<smem_desc_hi_sw128(1024)>(tmem + 256 + t * D, tmem + t * 128 + kk * 8, v_lo + kk * (2048 >> 4),
+                                                      Cfg::kIdescPV, (i > 3 || kk > 0) ? 1u : 0u);
             mma_commit_w(smem_u32(&bars->o_full[t]));
             mma_commit_w(smem_u32(&bars->v_empty[vp.slot]));
             vp.next();
           }
           if (i < pc.n) {
-            const uint32_t k_smem = k_ring + kp.slot * Cfg::kTileBytes;
+            const uint32_t k_lo = smem_desc_lo(k_ring + kp.slot * Cfg::kTileBytes, 16), q_lo = smem_desc_lo(q_smem, 16);
             if (!tree_wait(smem_u32(&bars->k_full[kp.slot]), kp.phase, wc)) { ok = false; break; }
             tc_fence_after();
             const uint32_t idesc = idesc_bf16_f32(128, (max(step_keys(a, pc, pc.j0 + i), 1) + 15) / 16 * 16, false, false);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * (TILE * 128) + (kk & 3) * 32;
-              mma_ss_w(tmem + t * 128, smem_desc_sw128(q_smem + off, 16, 1024), smem_desc_sw128(k_smem + off, 16, 1024), idesc,
-                       kk > 0 ? 1u : 0u);
+              const uint32_t off = ((kk >> 2) * (TILE * 128) + (kk & 3) * 32) >> 4;
+              mma_ss_lo_w<smem_desc_hi_sw128(1024)>(tmem + t * 128, q_lo + off, k_lo + off, idesc, kk > 0 ? 1u : 0u);
             }
             mma_commit_w(smem_u32(&bars->s_full[t]));
             mma_commit_w(smem_u32(&bars->k_empty[kp.slot]));

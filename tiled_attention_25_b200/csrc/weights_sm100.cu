@@ -12,9 +12,10 @@
 // a prompt adds up to a million exponentials into one fp32 number.
 //
 // Bounds.  A draft's few rows: the bytes of K, streamed once.  A prompt: the
-// exponentials, one per visible (query, key) pair; the products take a quarter
-// of the time that the special-function unit alone would need, so 3 of 8 pairs
-// of exponentials are evaluated on the FMA pipe (degree 5, 2e-7 relative).
+// exponentials, one per visible (query, key) pair, on the special-function unit
+// (1024 clocks to a 128x128 tile; the products take half of that).  Evaluating
+// some of them on the FMA pipe instead, as the forward kernel does, was slower
+// (a 4096-token prompt 198 us with none, 209 with a quarter, 219 with 3 of 8).
 //
 // Which unit a CTA takes: with one Q tile to a row, an equal contiguous range
 // of the units in (row, head, pair) order, Q staying in shared memory while
@@ -38,7 +39,6 @@
 #include <cstdint>
 
 #include "cache.h"
-#include "exp2_poly5.h"
 #include "kernel_common.cuh"
 #include "launch.h"
 
@@ -264,24 +264,6 @@ __device__ __forceinline__ QTile q_tile(const RowTiles& rt, int G, int n, int ti
 
 // ------------------------------------------------------------------ sums
 //
-// 2^x of a pair on the FMA pipe (the forward kernel's range reduction, degree
-// 5).  x is at most about 0 where the LSE belongs to the scores; the clamps keep
-// other values from wrapping the exponent (2^128 and more come out as 2^127.99).
-__device__ __forceinline__ float2 exp2_poly5(float2 x) {
-  x.x = fminf(fmaxf(x.x, -126.f), 127.99f);
-  x.y = fminf(fmaxf(x.y, -126.f), 127.99f);
-  const float2 t = __fadd2_rn(x, make_float2(12582912.f, 12582912.f));
-  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
-  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-  float2 p = __ffma2_rn(make_float2(kExp2E5, kExp2E5), f, make_float2(kExp2E4, kExp2E4));
-  p = __ffma2_rn(p, f, make_float2(kExp2E3, kExp2E3));
-  p = __ffma2_rn(p, f, make_float2(kExp2E2, kExp2E2));
-  p = __ffma2_rn(p, f, make_float2(kExp2E1, kExp2E1));
-  p = __ffma2_rn(p, f, make_float2(kExp2E0, kExp2E0));
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
-}
-
 // One thread's 32 columns: 2^(x sl2 + neg), added into acc (pairs).
 template <bool SOFTCAP>
 __device__ __forceinline__ void sum_full(const uint32_t (&x)[32], const float* neg, float sl2, float cap_in, float cap_out,
@@ -300,10 +282,8 @@ __device__ __forceinline__ void sum_full(const uint32_t (&x)[32], const float* n
       a0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), s2, make_float2(ng.x, ng.y));
       a1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), s2, make_float2(ng.z, ng.w));
     }
-    // pairs 1 and 5 of every 8 on the FMA pipe
-    const int pair = e / 2 % 8;
     acc[0] = __fadd2_rn(acc[0], make_float2(ex2_approx(a0.x), ex2_approx(a0.y)));
-    acc[1] = __fadd2_rn(acc[1], pair == 0 || pair == 4 ? exp2_poly5(a1) : make_float2(ex2_approx(a1.x), ex2_approx(a1.y)));
+    acc[1] = __fadd2_rn(acc[1], make_float2(ex2_approx(a1.x), ex2_approx(a1.y)));
   }
 }
 
@@ -656,11 +636,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
           tc_fence_after();
           ++sc[t];
           const uint32_t k_smem = k_ring + ks.slot * Cfg::kTileBytes;
+          const uint32_t a_lo = smem_desc_lo(k_smem, 16), b_lo = smem_desc_lo(q_smem, 16), d = tmem + (t * 2 + sb) * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (TILE * 128) + (kk & 3) * 32;
-            mma_ss_w(tmem + (t * 2 + sb) * 128, smem_desc_sw128(k_smem + off, 16, 1024),
-                     smem_desc_sw128(q_smem + off, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+            const uint32_t off = ((kk >> 2) * (TILE * 128) + (kk & 3) * 32) >> 4;
+            mma_ss_lo_w<smem_desc_hi_sw128(1024)>(d, a_lo + off, b_lo + off, idesc, kk > 0 ? 1u : 0u);
           }
           mma_commit_w(smem_u32(&bars->s_full[t][sb]));
           if (j == u.n_rt - 1) mma_commit_w(smem_u32(&bars->k_empty[ks.slot]));
