@@ -2,7 +2,8 @@
 interleavings of its warp roles (CPU only).
 
 Roles as in ``tiled_attention_25_b200/csrc/weights_sm100.cu``: the TMA warp
-publishes units and loads their one or two K tiles and the Q tiles; the column warps fill in each Q
+publishes units and loads the first K tile of each and its Q tiles, a second
+TMA warp the second K tile; the column warps fill in each Q
 slot's LSE and limits (one arrival here); the MMA warp forms the scores of one
 or two key tiles per Q tile into two buffers each; a warpgroup to each buffer sums
 them, and the two of a tile join their sums.  A Q tile may stay for the next
@@ -17,22 +18,25 @@ from protocol_sim import Sim
 
 
 COLS = 4  # slots of the columns' ring
+UNITS_AHEAD = 4  # units published ahead
 
 
 def roles(sim, units, kbufs, qslots, gathered=False):
     """units: (Q tiles, key tiles, new_q, keep_q)."""
     full, empty, drain = sim.full, sim.empty, sim.drain
-    for i in range(2):
+    for i in range(UNITS_AHEAD):
         sim.bar(f"unit_full{i}", 1)
-        sim.bar(f"unit_empty{i}", 6)
+        sim.bar(f"unit_empty{i}", 7)
+    for i in range(2):
         sim.bar(f"j_full{i}", 1)
         sim.bar(f"j_empty{i}", 1)
         for t in range(2):
             sim.bar(f"s_full{t}{i}", 1)
             sim.bar(f"s_empty{t}{i}", 1)
-    for i in range(kbufs):
-        sim.bar(f"k_full{i}", 1)
-        sim.bar(f"k_empty{i}", 1)
+    for t in range(2):
+        for i in range(kbufs[t]):
+            sim.bar(f"k_full{t}{i}", 1)
+            sim.bar(f"k_empty{t}{i}", 1)
     for i in range(qslots):
         sim.bar(f"q_full{i}", 1)
         sim.bar(f"q_empty{i}", 1)
@@ -48,16 +52,16 @@ def roles(sim, units, kbufs, qslots, gathered=False):
         def body():
             nonlocal kn, ql
             for it, u in enumerate(walk):
-                if not (yield empty(f"unit_empty{it & 1}", it >> 1)):
+                if not (yield empty(f"unit_empty{it % UNITS_AHEAD}", it // UNITS_AHEAD)):
                     return
-                sim.arrive(f"unit_full{it & 1}")
+                sim.arrive(f"unit_full{it % UNITS_AHEAD}")
                 if u is None:
                     return
-                n, tiles, new, _ = u
-                for _ in range(tiles if n else 0):
-                    if not (yield empty(f"k_empty{kn % kbufs}", kn // kbufs)):
+                n, _, new, _ = u
+                if n:
+                    if not (yield empty(f"k_empty0{kn % kbufs[0]}", kn // kbufs[0])):
                         return
-                    sim.load(f"k_full{kn % kbufs}")
+                    sim.load(f"k_full0{kn % kbufs[0]}")
                     kn += 1
                 for _ in range(0 if new else 1, 0 if gathered else n):
                     if not (yield empty(f"q_empty{ql % qslots}", ql // qslots)):
@@ -65,19 +69,36 @@ def roles(sim, units, kbufs, qslots, gathered=False):
                     sim.load(f"q_full{ql % qslots}")
                     ql += 1
         yield from body()
-        for s in range(kbufs):
-            if (uses := (kn + kbufs - 1 - s) // kbufs):
-                yield drain(f"k_full{s}", uses - 1)
+        for s in range(kbufs[0]):
+            if (uses := (kn + kbufs[0] - 1 - s) // kbufs[0]):
+                yield drain(f"k_full0{s}", uses - 1)
         for s in range(qslots):
             if (uses := (ql + qslots - 1 - s) // qslots):
                 yield drain(f"q_full{s}", uses - 1)
 
+    def tma2():
+        kn = 0
+        for it, u in enumerate(walk):
+            if not (yield full(f"unit_full{it % UNITS_AHEAD}", it // UNITS_AHEAD)):
+                break
+            sim.arrive(f"unit_empty{it % UNITS_AHEAD}")
+            if u is None:
+                break
+            if u[0] and u[1] > 1:
+                if not (yield empty(f"k_empty1{kn % kbufs[1]}", kn // kbufs[1])):
+                    break
+                sim.load(f"k_full1{kn % kbufs[1]}")
+                kn += 1
+        for s in range(kbufs[1]):
+            if (uses := (kn + kbufs[1] - 1 - s) // kbufs[1]):
+                yield drain(f"k_full1{s}", uses - 1)
+
     def columns():
         ql = 0
         for it, u in enumerate(walk):
-            if not (yield full(f"unit_full{it & 1}", it >> 1)):
+            if not (yield full(f"unit_full{it % UNITS_AHEAD}", it // UNITS_AHEAD)):
                 return
-            sim.arrive(f"unit_empty{it & 1}")
+            sim.arrive(f"unit_empty{it % UNITS_AHEAD}")
             if u is None:
                 return
             for _ in range(0 if u[2] else 1, u[0]):
@@ -90,11 +111,11 @@ def roles(sim, units, kbufs, qslots, gathered=False):
 
     def mma():
         def body():
-            kn, ql, sc = 0, 0, [0, 0]
+            kn, ql, sc = [0, 0], 0, [0, 0]
             for it, u in enumerate(walk):
-                if not (yield full(f"unit_full{it & 1}", it >> 1)):
+                if not (yield full(f"unit_full{it % UNITS_AHEAD}", it // UNITS_AHEAD)):
                     return
-                sim.arrive(f"unit_empty{it & 1}")
+                sim.arrive(f"unit_empty{it % UNITS_AHEAD}")
                 if u is None:
                     return
                 n, tiles, new, keep = u
@@ -106,18 +127,19 @@ def roles(sim, units, kbufs, qslots, gathered=False):
                     if not (yield full(f"{ring}{(ql - 1) % of}", (ql - 1) // of)):
                         return
                     for t in range(tiles):
-                        k = kn + t
-                        if j == 0 and not (yield full(f"k_full{k % kbufs}", k // kbufs)):
+                        k = kn[t]
+                        if j == 0 and not (yield full(f"k_full{t}{k % kbufs[t]}", k // kbufs[t])):
                             return
                         if not (yield empty(f"s_empty{t}{sc[t] & 1}", sc[t] >> 1)):
                             return
                         sim.commit(f"s_full{t}{sc[t] & 1}")
                         sc[t] += 1
                         if j == n - 1:
-                            sim.commit(f"k_empty{k % kbufs}")
+                            sim.commit(f"k_empty{t}{k % kbufs[t]}")
                     if j < n - 1 or not keep:
                         sim.commit(f"q_empty{(ql - 1) % qslots}")
-                kn += tiles
+                kn[0] += 1
+                kn[1] += tiles > 1
         yield from body()
         sim.commit("drain")
         yield drain("drain", 0)
@@ -125,9 +147,9 @@ def roles(sim, units, kbufs, qslots, gathered=False):
     def sums(t, sb):
         ql = sc = joins = 0
         for it, u in enumerate(walk):
-            if not (yield full(f"unit_full{it & 1}", it >> 1)):
+            if not (yield full(f"unit_full{it % UNITS_AHEAD}", it // UNITS_AHEAD)):
                 return
-            sim.arrive(f"unit_empty{it & 1}")
+            sim.arrive(f"unit_empty{it % UNITS_AHEAD}")
             if u is None:
                 return
             n, tiles, new, keep = u
@@ -155,7 +177,7 @@ def roles(sim, units, kbufs, qslots, gathered=False):
                     sim.arrive(f"j_empty{t}")
                 joins += 1
 
-    return {"tma": tma(), "columns": columns(), "mma": mma(),
+    return {"tma": tma(), "tma2": tma2(), "columns": columns(), "mma": mma(),
             **{f"sums{t}{sb}": sums(t, sb) for t in range(2) for sb in range(2)}}
 
 
@@ -169,7 +191,7 @@ UNITS = {
 
 
 @pytest.mark.parametrize("gathered", [False, True])
-@pytest.mark.parametrize("bufs", [(4, 2), (5, 1), (8, 4)])
+@pytest.mark.parametrize("bufs", [((2, 2), 2), ((3, 2), 1), ((3, 2), 2), ((4, 4), 4)])
 @pytest.mark.parametrize("name", sorted(UNITS))
 def test_weights_protocol_never_deadlocks_or_aliases(name, bufs, gathered):
     for seed in range(120):
@@ -179,12 +201,12 @@ def test_weights_protocol_never_deadlocks_or_aliases(name, bufs, gathered):
         assert sim.in_flight_at_exit == 0
 
 
-@pytest.mark.parametrize("role", ["tma", "columns", "mma", "sums00", "sums01", "sums11"])
+@pytest.mark.parametrize("role", ["tma", "tma2", "columns", "mma", "sums00", "sums01", "sums11"])
 def test_a_wait_that_runs_out_ends_every_role(role):
     for name in ("prompt", "draft", "half"):
         for at in range(20):
             for seed in range(8):
                 sim = Sim(seed)
-                stuck = sim.run(roles(sim, UNITS[name], 4, 2), give_up=(role, at))
+                stuck = sim.run(roles(sim, UNITS[name], (2, 2), 2), give_up=(role, at))
                 assert stuck is None, f"{role} wait {at}, seed {seed}: {stuck}"
                 assert sim.in_flight_at_exit == 0, f"{role} wait {at}, seed {seed}: {sim.pending_at_exit}"

@@ -28,9 +28,11 @@
 // Warp roles (640 threads): four warpgroups of exponentials and sums, two to
 // each key tile of the pair, which take its score buffers in turn (with one to a
 // tile, two warps to an SM quarter, the quarter issued 0.47 instructions a
-// clock: their latencies showed); warp 16 MMA issuer; warp 17 TMA producer,
-// which publishes the units; warps 18-19 the columns' LSE and limits, and, when
-// a path chooses the queries, the gather of their Q rows.
+// clock: their latencies showed); warp 16 MMA issuer; warp 17 publishes the
+// units and loads Q and the first tile of K, warp 19 the second (a copy from
+// pages of 64 rows takes a warp ~1400 clocks, as long as HBM takes for it);
+// warp 18 the columns' LSE and limits, and, when a path chooses the queries,
+// the gather of their Q rows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,10 +48,11 @@ namespace attn25 {
 
 namespace {
 
-constexpr int kSumWarps = 16, kMmaWarp = 16, kTmaWarp = 17, kColumnWarp = 18;  // and 19
-constexpr int kWThreads = 640;
-constexpr int kMetaThreads = 64;
+constexpr int kSumWarps = 16, kMmaWarp = 16, kTmaWarp = 17, kColumnWarp = 18, kTma2Warp = 19;
+constexpr int kWThreads = 20 * 32;  // five warps to an SM quarter: a sixth would leave 80 registers a thread
+constexpr int kLaneCols = TILE / 32;  // columns of a lane of the column warp
 constexpr int kColSlots = 4;
+constexpr int kUnits = 4;  // published ahead, so that the next head's Q is gathered in time
 
 constexpr int kMaxSplit = 8;  // CTAs of a cluster
 constexpr int kXStride = (kMaxSplit + 1) * TILE;  // sums of a key tile: the other warpgroup's, the other CTAs'
@@ -76,7 +79,7 @@ struct Unit {
 };
 
 struct WBarriers {
-  uint64_t unit_full[2], unit_empty[2];
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t k_full[12], k_empty[12];
   uint64_t q_full[4], q_empty[4];  // a Q slot's copies; its products are done
   // a Q tile's columns (and, with a path, its gathered rows); read.  A ring of its
@@ -87,21 +90,21 @@ struct WBarriers {
   uint64_t x_full[2], x_empty[2];  // a cluster's sums: written by the others (first CTA); read (the others)
   uint64_t drain;
   uint32_t tmem_base, abort_flag, never_set;
-  Unit unit[2];
-  int32_t min_lim[kColSlots][2];   // smallest limit of each half of a Q tile's columns
+  Unit unit[kUnits];
+  int32_t min_lim[kColSlots];   // smallest limit of a Q tile's columns
   alignas(16) float neg[kColSlots][TILE];  // -LSE log2 e of the columns
   alignas(16) int32_t lim[kColSlots][TILE];  // the slots below the column's limit are the ones it sees
 };
 static_assert(sizeof(WBarriers) <= 6144, "barrier block");
 
-constexpr int kUnitReaders = kSumWarps + 3;  // and the MMA and column warps
+constexpr int kUnitReaders = kSumWarps + 3;  // and the MMA, column and second TMA warps
 
 struct WParams {
   WeightsArgs a;
   RowTiles rt;
   bool one_tile;  // every row's queries fit one Q tile
   int split;      // CTAs of a cluster that share a unit
-  int q_slots, k_slots;
+  int q_slots, k_slots[2], q_stride;  // slots of each key tile's ring; bytes between Q slots
   uint32_t head_magic;  // row / head_tile = row * head_magic >> 16 (rows below 128)
   uint64_t wait_ns;
 };
@@ -301,6 +304,50 @@ __device__ __forceinline__ void sum_limited(const uint32_t (&x)[32], const float
   }
 }
 
+// Load key tile t of a unit into its ring (the second follows the first's
+// slots).  false: a wait ran out.
+template <int D>
+__device__ __forceinline__ bool load_k(const WParams& p, const Unit& u, int t, const CUtensorMap* map, uint32_t k_ring,
+                                       WBarriers* bars, SlotPos& kp, int& copies, const WaitCtl& wc) {
+  const WeightsArgs& a = p.a;
+  const int s0 = u.kp * 2 * TILE + t * TILE;
+  if (u.n_rt == 0 || s0 >= u.len) return true;
+  const int lane = threadIdx.x & 31, ps = a.c.ix.page_size, box_rows = ps < TILE ? ps : TILE;
+  const int boxes = (min(TILE, u.len - s0) + box_rows - 1) / box_rows;
+  int entry = 0;  // of the tile's page `lane` (at most 8)
+  if (lane < boxes) {
+    const long long e = static_cast<long long>(u.b) * a.c.ix.max_pages + (s0 + lane * box_rows) / ps;
+    entry = a.c.ix.table != nullptr ? __ldg(a.c.ix.table + e) : static_cast<int>(e);
+  }
+  const int y = ps > TILE ? s0 % ps : 0, slot = (t == 0 ? 0 : p.k_slots[0]) + kp.slot;
+  const uint32_t bar = smem_u32(&bars->k_full[slot]), dst = k_ring + slot * WCfg<D>::kTileBytes;
+  if (!w_wait(smem_u32(&bars->k_empty[slot]), kp.phase ^ 1, wc)) return false;
+  if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
+  for (int i = 0; i < boxes; ++i) {
+    int page = __shfl_sync(0xffffffffu, entry, i);
+    const bool outside = page < 0 || page >= a.c.ix.num_pages;
+    if (outside) page = a.c.ix.num_pages;  // past the pool: the copy fills in zeros
+    if (lane == 0) {
+      if (outside) flag_index(a.c.status);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_4d(dst + c * (TILE * 128) + i * box_rows * 128, map, bar, c * 64, y, u.hk, page);
+    }
+  }
+  __syncwarp();
+  kp.next(p.k_slots[t]);
+  ++copies;
+  return true;
+}
+
+// Let a ring's last copies land before the CTA exits (one thread).
+__device__ __forceinline__ void drain_slots(uint64_t* full, int slots, int copies, const WaitCtl& wc) {
+  for (int s = 0; s < slots; ++s) {
+    const int uses = (copies + slots - 1 - s) / slots;
+    if (uses > 0) mbar_wait_thread(smem_u32(full + s), (uses - 1) & 1, wc);
+  }
+}
+
 template <int D, bool SOFTCAP>
 __global__ void __launch_bounds__(kWThreads, 1)
     cache_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -311,15 +358,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   WBarriers* bars = reinterpret_cast<WBarriers*>(smem + Cfg::kBarOff);
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t k_ring = sbase + p.q_slots * Cfg::kTileBytes;
+  const uint32_t k_ring = sbase + (p.one_tile ? 1 : p.q_slots) * Cfg::kTileBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cta_rank()) : 0;
   const int walkers = gridDim.x / p.split, walker = blockIdx.x / p.split;  // clusters walk together
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kUnits; ++i) {
       mbar_init(smem_u32(&bars->unit_full[i]), 1);
       mbar_init(smem_u32(&bars->unit_empty[i]), kUnitReaders);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->j_full[i]), 4);
       mbar_init(smem_u32(&bars->j_empty[i]), 4);
       mbar_init(smem_u32(&bars->x_full[i]), max(1, (p.split - 1) * TILE));  // (unused where split is 1)
@@ -338,7 +387,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(smem_u32(&bars->q_empty[i]), 1);
     }
     for (int i = 0; i < kColSlots; ++i) {
-      mbar_init(smem_u32(&bars->c_full[i]), kMetaThreads);
+      mbar_init(smem_u32(&bars->c_full[i]), 32);
       mbar_init(smem_u32(&bars->c_empty[i]), kSumWarps);
     }
     mbar_init(smem_u32(&bars->drain), 1);
@@ -347,10 +396,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     fence_mbar_init();
   }
   // rows that no Q tile fills stay zero (their columns' sums then add 2^-inf)
+  const int room = p.one_tile && p.q_slots == 2 ? 64 : TILE;  // rows of a slot
   for (int s = 0; s < p.q_slots; ++s)
-    for (int i = threadIdx.x; i < (TILE - p.rt.rows) * (D / 8); i += kWThreads) {
+    for (int i = threadIdx.x; i < (room - p.rt.rows) * (D / 8); i += kWThreads) {
       const int row = p.rt.rows + i / (D / 8), ch = i % (D / 8);
-      *reinterpret_cast<uint4*>(smem + s * Cfg::kTileBytes + (ch >> 3) * (TILE * 128) + row * 128 + (ch & 7) * 16) =
+      *reinterpret_cast<uint4*>(smem + s * p.q_stride + (ch >> 3) * (TILE * 128) + row * 128 + (ch & 7) * 16) =
           make_uint4(0u, 0u, 0u, 0u);
     }
   fence_proxy_async_smem();
@@ -371,8 +421,6 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ TMA producer
-    const int ps = a.c.ix.page_size;
-    const int box_rows = ps < TILE ? ps : TILE;
     WScan scan;
     w_load(scan, a, 0);
     const long long total = units_below(scan, a, INT_MAX);
@@ -410,7 +458,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       next = nth(walker);
     }
     SlotPos kp, qp;
-    uint32_t k_copies = 0, q_copies = 0;
+    int k_copies = 0, q_copies = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
       Unit u = next;
@@ -436,47 +484,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
           if (v < total) next = nth(v);
         }
       }
-      const int buf = it & 1;
-      if (!w_wait(smem_u32(&bars->unit_empty[buf]), ((it >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+      const int buf = it % kUnits;
+      if (!w_wait(smem_u32(&bars->unit_empty[buf]), ((it / kUnits) & 1) ^ 1, wc)) { ok = false; break; }
       if (lane == 0) {
         bars->unit[buf] = u;
         mbar_arrive(smem_u32(&bars->unit_full[buf]));
       }
       __syncwarp();
       if (u.b < 0) break;
-      if (u.n_rt > 0) {
-        // K of one or two tiles: the pages that hold filled slots, looked up for both at once
-        const int s0 = u.kp * 2 * TILE, used = min(2 * TILE, u.len - s0), boxes = (used + box_rows - 1) / box_rows;
-        const int per_tile = TILE / box_rows;
-        int entry = 0;  // of page `lane` of the pair
-        if (lane < boxes) {
-          const long long e = static_cast<long long>(u.b) * a.c.ix.max_pages + (s0 + lane * box_rows) / ps;
-          entry = a.c.ix.table != nullptr ? __ldg(a.c.ix.table + e) : static_cast<int>(e);
-        }
-        const int y0 = ps > TILE ? s0 % ps : 0;  // (a pair may end in the next page)
-        for (int t = 0; t < 2 && t * TILE < used; ++t) {
-          if (!w_wait(smem_u32(&bars->k_empty[kp.slot]), kp.phase ^ 1, wc)) { ok = false; break; }
-          const uint32_t bar = smem_u32(&bars->k_full[kp.slot]), dst = k_ring + kp.slot * Cfg::kTileBytes;
-          const int end = min(boxes, (t + 1) * per_tile);
-          if (lane == 0) mbar_arrive_expect_tx(bar, (end - t * per_tile) * box_rows * D * 2);
-          for (int i = t * per_tile; i < end; ++i) {
-            int page = __shfl_sync(0xffffffffu, entry, i);
-            const bool outside = page < 0 || page >= a.c.ix.num_pages;
-            if (outside) page = a.c.ix.num_pages;  // past the pool: the copy fills in zeros
-            if (lane == 0) {
-              if (outside) flag_index(a.c.status);
-              const int y = ps > TILE ? (y0 + t * TILE) % ps : 0;
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_4d(dst + c * (TILE * 128) + (i - t * per_tile) * box_rows * 128, &tm_k, bar, c * 64, y, u.hk, page);
-            }
-          }
-          __syncwarp();
-          kp.next(p.k_slots);
-          ++k_copies;
-        }
-        if (!ok) break;
-      }
+      if (!load_k<D>(p, u, 0, &tm_k, k_ring, bars, kp, k_copies, wc)) { ok = false; break; }
       // Q tiles (with a path the column warps gather them instead)
       for (int j = u.new_q ? 0 : 1; a.path == nullptr && j < u.n_rt; ++j) {
         if (!w_wait(smem_u32(&bars->q_empty[qp.slot]), qp.phase ^ 1, wc)) { ok = false; break; }
@@ -486,7 +502,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           mbar_arrive_expect_tx(bar, p.rt.rows * D * 2);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sbase + qp.slot * Cfg::kTileBytes + c * (TILE * 128), &tm_q, bar, c * 64, u.hk * a.G + q.h0, q.i0, u.b);
+            tma_load_4d(sbase + qp.slot * p.q_stride + c * (TILE * 128), &tm_q, bar, c * 64, u.hk * a.G + q.h0, q.i0, u.b);
         }
         __syncwarp();
         qp.next(p.q_slots);
@@ -495,51 +511,59 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
     if (lane == 0) {  // let the copies in flight land before the CTA exits
       const WaitCtl drain_wc{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status};
-      for (int s = 0; s < p.k_slots; ++s) {
-        const int uses = (static_cast<int>(k_copies) + p.k_slots - 1 - s) / p.k_slots;
-        if (uses > 0) mbar_wait_thread(smem_u32(&bars->k_full[s]), (uses - 1) & 1, drain_wc);
-      }
-      for (int s = 0; s < p.q_slots; ++s) {
-        const int uses = (static_cast<int>(q_copies) + p.q_slots - 1 - s) / p.q_slots;
-        if (uses > 0) mbar_wait_thread(smem_u32(&bars->q_full[s]), (uses - 1) & 1, drain_wc);
-      }
+      drain_slots(bars->k_full, p.k_slots[0], k_copies, drain_wc);
+      drain_slots(bars->q_full, p.q_slots, q_copies, drain_wc);
     }
-  } else if (warp >= kColumnWarp) {
-    // ------------------------------------------------------------ columns of the Q tiles
-    const int m = threadIdx.x - kColumnWarp * 32;
-    SlotPos qp, cp;
+  } else if (warp == kTma2Warp) {
+    // ------------------------------------------------------------ second K tiles
+    SlotPos kp;
+    int copies = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      const int buf = it & 1;
-      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
+      const int buf = it % kUnits;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it / kUnits) & 1, wc)) break;
       const Unit u = bars->unit[buf];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
       if (u.b < 0) break;
-      // this thread's two columns of tile j: read one tile ahead, looked at when it is published
-      float lse[2] = {};
-      int lim[2] = {};
-      bool real[2] = {};
+      ok = load_k<D>(p, u, 1, &tm_k, k_ring, bars, kp, copies, wc);
+    }
+    if (lane == 0)
+      drain_slots(bars->k_full + p.k_slots[0], p.k_slots[1], copies,
+                  WaitCtl{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status});
+  } else if (warp == kColumnWarp) {
+    // ------------------------------------------------------------ columns of the Q tiles
+    SlotPos qp, cp;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      const int buf = it % kUnits;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it / kUnits) & 1, wc)) break;
+      const Unit u = bars->unit[buf];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
+      if (u.b < 0) break;
+      // this lane's columns (lane + 32 x) of tile j: read one tile ahead, looked at when it is published
+      float lse[kLaneCols] = {};
+      int lim[kLaneCols] = {}, node[kLaneCols] = {};  // node -1: no query
       auto fetch = [&](int j) {
         const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = m + 64 * x, r_tok = static_cast<int>(r * p.head_magic >> 16), i = q.i0 + r_tok;
+        for (int x = 0; x < kLaneCols; ++x) {
+          const int r = lane + 32 * x, r_tok = static_cast<int>(r * p.head_magic >> 16), i = q.i0 + r_tok;
           const int head = q.h0 + r - r_tok * p.rt.head_tile;
-          int node = i;
-          real[x] = r < p.rt.rows && i < u.n && head < a.G;
-          if (real[x] && a.path != nullptr) {
-            node = a.path[static_cast<long long>(u.b) * a.T + i];
-            if (node < 0 || node >= a.T) {
-              real[x] = false;
+          node[x] = r < p.rt.rows && i < u.n && head < a.G ? i : -1;
+          if (node[x] >= 0 && a.path != nullptr) {
+            node[x] = a.path[static_cast<long long>(u.b) * a.T + i];
+            if (node[x] < 0 || node[x] >= a.T) {
+              node[x] = -1;
               flag_index(a.c.status);
             }
           }
           // what no query fills holds zeros behind the tile's rows and where rows are
           // gathered: its column adds 2^-inf; elsewhere it may hold anything and is left out
           const bool zeros = r >= p.rt.rows || a.path != nullptr;
-          lim[x] = real[x] ? u.len - u.n + i + 1 : (zeros ? INT_MAX : 0);
-          if (real[x]) lse[x] = __ldg(a.lse + (static_cast<long long>(u.b) * a.Hq + u.hk * a.G + head) * a.T + node);
+          lim[x] = node[x] >= 0 ? u.len - u.n + i + 1 : (zeros ? INT_MAX : 0);
+          if (node[x] >= 0) lse[x] = __ldg(a.lse + (static_cast<long long>(u.b) * a.Hq + u.hk * a.G + head) * a.T + node[x]);
         }
       };
       const int j0 = u.new_q ? 0 : 1;
@@ -548,38 +572,54 @@ __global__ void __launch_bounds__(kWThreads, 1)
       for (int j = j0; j < u.n_rt; ++j) {
         const int slot = cp.slot;
         const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
-        const float lse_now[2] = {lse[0], lse[1]};
-        const int lim_now[2] = {lim[0], lim[1]};
-        const bool real_now[2] = {real[0], real[1]};
-        if (j + 1 < u.n_rt) fetch(j + 1);
-        int low = INT_MAX;
+        float lse_now[kLaneCols];
+        int lim_now[kLaneCols], node_now[kLaneCols], low = INT_MAX;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (m + 64 * x < q.cols) low = min(low, lim_now[x]);
+        for (int x = 0; x < kLaneCols; ++x) {
+          lse_now[x] = lse[x];
+          lim_now[x] = lim[x];
+          node_now[x] = node[x];
+          if (lane + 32 * x < q.cols) low = min(low, lim[x]);
+        }
+        if (j + 1 < u.n_rt) fetch(j + 1);
         low = __reduce_min_sync(0xffffffffu, low);
         if (!w_wait(smem_u32(&bars->c_empty[slot]), cp.phase ^ 1, wc)) { ok = false; break; }
-        if (lane == 0) bars->min_lim[slot][warp - kColumnWarp] = low;
+        if (lane == 0) bars->min_lim[slot] = low;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          bars->neg[slot][m + 64 * x] = real_now[x] ? -lse_now[x] * LOG2E : -INFINITY;
-          bars->lim[slot][m + 64 * x] = lim_now[x];
+        for (int x = 0; x < kLaneCols; ++x) {
+          bars->neg[slot][lane + 32 * x] = node_now[x] >= 0 ? -lse_now[x] * LOG2E : -INFINITY;
+          bars->lim[slot][lane + 32 * x] = lim_now[x];
         }
         if (a.path != nullptr) {
-          // the chosen queries' rows, in the 128-byte swizzle: chunk c of row r at c ^ (r & 7)
+          // the chosen queries' rows, in the 128-byte swizzle (chunk c of row r at
+          // c ^ (r & 7))
           if (!w_wait(smem_u32(&bars->q_empty[qp.slot]), qp.phase ^ 1, wc)) { ok = false; break; }
-          uint8_t* dst = smem + qp.slot * Cfg::kTileBytes;
-#pragma unroll 4
-          for (int x = m; x < q.cols * (D / 8); x += kMetaThreads) {
-            const int r = x / (D / 8), ch = x % (D / 8), r_tok = static_cast<int>(r * p.head_magic >> 16), i = q.i0 + r_tok,
-                      head = q.h0 + r - r_tok * p.rt.head_tile;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < q.rows && head < a.G) {
-              const int node = a.path[static_cast<long long>(u.b) * a.T + i];
-              if (node >= 0 && node < a.T)
-                v = __ldg(reinterpret_cast<const uint4*>(a.q + u.b * a.q_st.b + (u.hk * a.G + head) * a.q_st.h +
-                                                         node * a.q_st.s + ch * 8));
+          uint8_t* dst = smem + qp.slot * p.q_stride;
+          constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // chunks of a row, rows of a pass
+          const int ch = lane % kChunks, sub = lane / kChunks;
+#pragma unroll
+          for (int x = 0; x < kLaneCols; ++x) {
+            const int base = 32 * x;
+            if (base >= q.cols) continue;
+            // all loads of a batch before its stores
+            constexpr int kBatch = 8;
+#pragma unroll 1
+            for (int y0 = 0; y0 < 32; y0 += kBatch * kRows) {
+              uint4 v[kBatch];
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                const int y = y0 + e * kRows + sub, r = base + y, r_tok = static_cast<int>(r * p.head_magic >> 16);
+                const int n = __shfl_sync(0xffffffffu, node_now[x], y & 31);
+                const long long at = u.b * a.q_st.b + (u.hk * a.G + q.h0 + r - r_tok * p.rt.head_tile) * a.q_st.h + n * a.q_st.s;
+                v[e] = __ldg(reinterpret_cast<const uint4*>(a.q + (n >= 0 ? at : 0) + ch * 8));
+                if (n < 0) v[e] = make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e) {
+                const int r = base + y0 + e * kRows + sub;
+                *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[e];
+              }
             }
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (TILE * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
           }
           fence_proxy_async_smem();
           qp.next(p.q_slots);
@@ -590,23 +630,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    SlotPos kp, qp, cp, cur, cols;  // cur, cols: the Q and column slots in use
+    SlotPos kp[2], qp, cp, cur, cols;  // cur, cols: the Q and column slots in use
     uint32_t sc[2] = {0, 0};
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      const int buf = it & 1;
-      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
+      const int buf = it % kUnits;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it / kUnits) & 1, wc)) break;
       const Unit u = bars->unit[buf];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
       if (u.b < 0) break;
       if (u.n_rt == 0) continue;
       const int tiles = u.len - u.kp * 2 * TILE > TILE ? 2 : 1;
-      SlotPos kt[2];
-      for (int t = 0; t < tiles; ++t) {
-        kt[t] = kp;
-        kp.next(p.k_slots);
-      }
 #pragma unroll 1
       for (int j = 0; j < u.n_rt && ok; ++j) {
         if (j > 0 || u.new_q) {
@@ -623,19 +658,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
         const uint32_t idesc = idesc_bf16_f32(128, q.cols, false, false);
-        const uint32_t q_smem = sbase + cur.slot * Cfg::kTileBytes;
+        const uint32_t q_smem = sbase + cur.slot * p.q_stride;
 #pragma unroll 1
         for (int t = 0; t < tiles; ++t) {
           const int sb = sc[t] & 1;
-          const SlotPos ks = t == 0 ? kt[0] : kt[1];
-          if ((j == 0 && !w_wait(smem_u32(&bars->k_full[ks.slot]), ks.phase, wc)) ||
+          const int k_slot = t == 0 ? kp[0].slot : p.k_slots[0] + kp[1].slot;
+          if ((j == 0 && !w_wait(smem_u32(&bars->k_full[k_slot]), t == 0 ? kp[0].phase : kp[1].phase, wc)) ||
               !w_wait(smem_u32(&bars->s_empty[t][sb]), ((sc[t] >> 1) & 1) ^ 1, wc)) {
             ok = false;
             break;
           }
           tc_fence_after();
           ++sc[t];
-          const uint32_t k_smem = k_ring + ks.slot * Cfg::kTileBytes;
+          const uint32_t k_smem = k_ring + k_slot * Cfg::kTileBytes;
           const uint32_t a_lo = smem_desc_lo(k_smem, 16), b_lo = smem_desc_lo(q_smem, 16), d = tmem + (t * 2 + sb) * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -643,10 +678,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
             mma_ss_lo_w<smem_desc_hi_sw128(1024)>(d, a_lo + off, b_lo + off, idesc, kk > 0 ? 1u : 0u);
           }
           mma_commit_w(smem_u32(&bars->s_full[t][sb]));
-          if (j == u.n_rt - 1) mma_commit_w(smem_u32(&bars->k_empty[ks.slot]));
+          if (j == u.n_rt - 1) mma_commit_w(smem_u32(&bars->k_empty[k_slot]));
         }
         if (ok && (j < u.n_rt - 1 || !u.keep_q)) mma_commit_w(smem_u32(&bars->q_empty[cur.slot]));
       }
+      kp[0].next(p.k_slots[0]);
+      if (tiles > 1) kp[1].next(p.k_slots[1]);
     }
     mma_commit_w(smem_u32(&bars->drain));
     w_wait(smem_u32(&bars->drain), 0, WaitCtl{drain_limit(p.wait_ns), smem_u32(&bars->never_set), a.c.status});
@@ -662,8 +699,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     float* x_buf = reinterpret_cast<float*>(smem + Cfg::kXOff) + t * kXStride;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      const int buf = it & 1;
-      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it >> 1) & 1, wc)) break;
+      const int buf = it % kUnits;
+      if (!w_wait(smem_u32(&bars->unit_full[buf]), (it / kUnits) & 1, wc)) break;
       const Unit u = bars->unit[buf];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->unit_empty[buf]));
@@ -690,7 +727,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             const QTile q = q_tile(p.rt, a.G, u.n, u.rt0 + j * p.split);
             if (!w_wait(smem_u32(&bars->s_full[t][sb]), (sc >> 1) & 1, wc)) { ok = false; break; }
             tc_fence_after();
-            const bool full = min(bars->min_lim[slot][0], bars->min_lim[slot][1]) >= key0 + TILE;
+            const bool full = bars->min_lim[slot] >= key0 + TILE;
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
             for (int c = 0; c < q.cols; c += 32) {
@@ -782,8 +819,13 @@ cudaError_t launch_cache_weights(const CUtensorMap& tq, const CUtensorMap& tk, c
   p.rt = row_tiles(a.G, a.T);
   p.one_tile = p.rt.tiles == 1;
   const int q_slots = a.c.D == 128 ? WCfg<128>::kQSlots : WCfg<64>::kQSlots, tiles = a.c.D == 128 ? WCfg<128>::kTiles : WCfg<64>::kTiles;
-  p.q_slots = p.one_tile ? 1 : q_slots;
-  p.k_slots = tiles - p.q_slots;
+  // one Q tile to a row: one slot's room for it, which holds two tiles of up to 64 rows
+  const bool two = p.one_tile && p.rt.rows <= 64;
+  p.q_slots = p.one_tile ? (two ? 2 : 1) : q_slots;
+  p.q_stride = two ? 64 * 128 : TILE * a.c.D * 2;
+  const int k_slots = tiles - (p.one_tile ? 1 : q_slots);
+  p.k_slots[0] = (k_slots + 1) / 2;
+  p.k_slots[1] = k_slots / 2;
   // a prompt's units (its new tokens alone): shared while they fill less than half the SMs
   p.split = 1;
   if (!p.one_tile) {
