@@ -420,8 +420,10 @@ ATTN25_API int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new
  * and the accepted ones go in with attn_cache_append.  k_new and v_new both
  * NULL: the queries see the cache alone (parents must be NULL); a query of a
  * row with no filled slot then gets O = 0 and LSE = -inf.  Rows t >=
- * counts[b] of out and lse are left as they were.  A parent outside
- * [-1, t) counts as -1 (ATTN_ERR_INDEX).
+ * counts[b] of out and lse are left as they were, and such rows of q, k_new
+ * and v_new may hold anything.  (As in attn_fwd, an infinite or NaN value of
+ * a real token reaches the rows of its tile that do not see it.)  A parent
+ * outside [-1, t) counts as -1 (ATTN_ERR_INDEX).
  * mod_kind: ATTN_MOD_NONE or ATTN_MOD_SOFTCAP (slots of a cache that has
  * evicted some have no index to mask by; ATTN_ERR_UNSUPPORTED otherwise).
  * workspace: device memory of at least attn_tree_workspace_size bytes,

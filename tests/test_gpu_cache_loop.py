@@ -95,3 +95,54 @@ def test_serving_rounds(D, Hq, Hkv, page):
                     assert set(range(int(seen[b]) - recent, int(seen[b]))) <= set(pos[b, h, :n].tolist())
     assert evicted > 0 and (lens == budget).all()
     assert ta.attn_get_status() == 0
+
+
+def test_a_captured_round_replays_like_the_eager_one():
+    """One decode round, all operators in place, as a graph: replays advance the
+    cache exactly as the same calls do eagerly."""
+    import tiled_attention_25_b200 as ta
+    B, Hq, Hkv, D, T, budget = 2, 8, 2, 64, 4, 40
+    rng = np.random.default_rng(5)
+    tokens = [dev16(bf16(rng.standard_normal((B, Hq, T, D)))[0]) for _ in range(3)]
+    k_new, v_new = (dev16(bf16(rng.standard_normal((B, Hkv, T, D)))[0]) for _ in range(2))
+    path, accepted = i32([[0, 2, 3, 0], [0, 1, 0, 0]]), i32([3, 2])
+    parents = i32([[-1, 0, 0, 2], [-1, 0, 1, 1]])
+
+    def setup():
+        cache = ta.new_attn_cache(B, Hkv, 64, D, page_size=16)
+        cache.k.zero_()
+        cache.v.zero_()
+        st = dict(cache=cache, q=torch.empty_like(tokens[0]), out=torch.zeros_like(tokens[0]),
+                  lse=torch.zeros(B, Hq, T, device="cuda"), w=torch.zeros(B, Hkv, 64, device="cuda"),
+                  pos=torch.zeros(B, Hkv, 64, dtype=torch.int32, device="cuda"), seen=i32([0, 0]),
+                  moves=torch.zeros(B, Hkv, budget, 2, dtype=torch.int32, device="cuda"),
+                  n=torch.zeros(B, Hkv, dtype=torch.int32, device="cuda"), ws=ta.new_tree_workspace(Hq, Hkv, T, D))
+        return st
+
+    def step(s):
+        ta.attn_tree_fwd(s["q"], k_new, v_new, s["cache"], s["out"], s["lse"], s["ws"], parents=parents)
+        ta.attn_cache_append(s["cache"], k_new, v_new, path=path, counts=accepted, positions=s["pos"], seen=s["seen"])
+        ta.attn_cache_weights(s["q"], s["lse"], s["cache"], s["w"], s["w"], path=path, counts=accepted)
+        s["seen"] += accepted
+        ta.attn_evict_plan(s["cache"], s["w"], s["pos"], s["seen"], s["moves"], s["n"], budget, 1, 8)
+        ta.attn_cache_compact(s["cache"], s["moves"], s["n"], budget, weights=s["w"], positions=s["pos"])
+
+    eager, captured = setup(), setup()
+    warm = setup()
+    warm["q"].copy_(tokens[0])
+    step(warm)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(captured)
+    for i in range(24):
+        for s in (eager, captured):
+            s["q"].copy_(tokens[i % 3])
+        step(eager)
+        g.replay()
+        torch.cuda.synchronize()
+        for name in ("out", "lse", "w", "pos", "seen", "moves", "n"):
+            assert torch.equal(eager[name], captured[name]), (i, name)
+        for name in ("k", "v", "lens"):
+            assert torch.equal(getattr(eager["cache"], name), getattr(captured["cache"], name)), (i, name)
+    assert (eager["cache"].lens == budget).all() and ta.attn_get_status() == 0

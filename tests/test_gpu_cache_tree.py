@@ -76,6 +76,48 @@ def test_ragged_counts(ta, T):
     run_and_check(ta, c, random_tree(rng, 5, T), f"T={T}")
 
 
+@pytest.mark.parametrize("Hq,Hkv,T", [(40, 1, 1024), (2, 1, 1024), (100, 2, 130)])
+def test_more_query_tiles_than_sms(ta, Hq, Hkv, T):
+    """342 tiles, one to a CTA; two; tiles whose tokens only some rows have."""
+    c = CacheCase(T + Hq, [70, 3], Hq, Hkv, 64, 64, T, counts=[T, T // 3])
+    run_and_check(ta, c, random_tree(c.rng, 2, T) if T < 1000 else None, f"heads {Hq}/{Hkv} T={T}")
+
+
+def test_no_queries_at_all(ta):
+    c = CacheCase(4, [300, 0], 4, 2, 128, 64, 3, counts=[0, 0])
+    run_and_check(ta, c, None)
+
+
+def test_more_rows_than_one_window(ta):
+    """130 rows: items above and below the number of SMs, rows without queries among them."""
+    rng = np.random.default_rng(21)
+    for lens, Hkv in ((rng.integers(0, 40, 130), 1), (rng.integers(0, 700, 100), 2)):
+        counts = rng.integers(0, 3, len(lens))
+        c = CacheCase(22, lens, 2 * Hkv, Hkv, 64, 16, 2, counts)
+        run_and_check(ta, c, random_tree(rng, len(lens), 2))
+
+
+def test_cuts_of_many_items(ta):
+    """More items than SMs, some long, so that the stream is cut inside and near the ends of items."""
+    rng = np.random.default_rng(23)
+    lens = [int(x) for x in rng.integers(1, 200, 36)] + [9000, 5000, 1200, 640]
+    c = CacheCase(24, lens, 8, 4, 64, 128, 2)
+    a, la = run_and_check(ta, c, None)
+    b, lb = call(ta, c, None)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_one_workspace_serves_other_shapes(ta):
+    """The counters at its head are zero after every call."""
+    ws = ta.new_tree_workspace(32, 1, 64, 128)
+    for seed, (lens, Hq, Hkv, D, T) in enumerate([([3000], 8, 1, 128, 3), ([900, 4000], 4, 2, 64, 20), ([6000], 32, 1, 64, 4)]):
+        c = CacheCase(30 + seed, lens, Hq, Hkv, D, 64, T)
+        out, lse = call(ta, c, None, ws=ws)
+        torch.cuda.synchronize()
+        check_tree(out, lse, tree_reference(c, None), str(lens))
+        assert (ws[:1024] == 0).all()
+
+
 def test_every_root_and_a_deep_chain(ta):
     """All nodes siblings (no one sees another), and one path through all."""
     c = CacheCase(5, [70, 128], 4, 1, 128, 64, 60)

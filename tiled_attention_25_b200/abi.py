@@ -510,9 +510,9 @@ class AttnCache:
     def __init__(self, k, v, lens, page_table=None):
         if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("k and v must be [pages][Hkv][page_size][D] pools of one shape")
-        self.device = k.device
         if not k.is_cuda:
             raise ValueError("k and v must be CUDA tensors")
+        self.device, self._index = k.device, k.get_device()
         P, Hkv, page, D = k.shape
         B = lens.shape[0] if lens.dim() == 1 else 0
         self._own(lens, torch.int32, (B,), "lens")
@@ -537,7 +537,7 @@ class AttnCache:
         its pointer (None stays None)."""
         if t is None:
             return None
-        if t.dtype != dtype or t.device != self.device:
+        if t.dtype is not dtype or t.get_device() != self._index:
             raise ValueError(f"{what} must be a {dtype} tensor on the cache's CUDA device")
         if shape is not None and (t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor")
@@ -551,7 +551,7 @@ class AttnCache:
             if t is None:
                 ptrs.append(None)
                 continue
-            if t.dtype != torch.bfloat16 or t.device != self.device or t.shape != shape:
+            if t.dtype is not torch.bfloat16 or t.get_device() != self._index or t.shape != shape:
                 raise ValueError(f"{name} must be a bf16 {tuple(shape)} view on the cache's device")
             ptrs.append(t.data_ptr())
             if lay is None and not t.is_contiguous():
@@ -565,7 +565,7 @@ class AttnCache:
     def _call(self, name, fn, stream, *args):
         """The C call with the cache's device current, on `stream` (default:
         that device's current stream)."""
-        dev = self.device.index
+        dev = self._index
         if stream is None:
             raw = torch._C._cuda_getCurrentRawStream(dev)  # current_stream(dev).cuda_stream without a Stream object
         else:

@@ -2,6 +2,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "cache.h"
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   if (n > a.budget) {  // the same for the whole cluster
     const float* w = a.weights + static_cast<long long>(bh) * a.ix.capacity;
     const int32_t* pos = a.positions + static_cast<long long>(bh) * a.ix.capacity;
-    const int recent_from = a.seen[b] - a.recent;
+    const int recent_from = static_cast<int>(max(static_cast<long long>(a.seen[b]) - a.recent, static_cast<long long>(INT_MIN)));
     // this CTA's slots [j0, j0 + m) in quads of four
     const int share = ((n + ctas - 1) / ctas + 31) / 32 * 32;
     const int j0 = min(n, rank * share), m = min(n - j0, share), quads = (m + 3) / 4;
