@@ -721,11 +721,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             tc_fence_after();
             const uint32_t v_lo = smem_desc_lo(v_ring + vp.slot * Cfg::kTileBytes, TILE * 128);
             const int kks = (max(step_keys(a, pc, pc.j0 + i - 2), 1) + 15) / 16;
+            const uint32_t o_tm = tmem + 256 + t * D, p_tm = tmem + t * 128, first = i > 3 ? 1u : 0u;
+            // (a full step's 8 products without a branch before each: 480 clocks to issue, not 850)
+            if (kks == TILE / 16) {
 #pragma unroll
-            for (int kk = 0; kk < TILE / 16; ++kk)
-              if (kk < kks)
-                mma_ts_lo_w<smem_desc_hi_sw128(1024)>(tmem + 256 + t * D, tmem + t * 128 + kk * 8, v_lo + kk * (2048 >> 4),
-                                                      Cfg::kIdescPV, (i > 3 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < TILE / 16; ++kk)
+                mma_ts_lo_w<smem_desc_hi_sw128(1024)>(o_tm, p_tm + kk * 8, v_lo + kk * (2048 >> 4), Cfg::kIdescPV,
+                                                      kk > 0 ? 1u : first);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < kks; ++kk)
+                mma_ts_lo_w<smem_desc_hi_sw128(1024)>(o_tm, p_tm + kk * 8, v_lo + kk * (2048 >> 4), Cfg::kIdescPV,
+                                                      kk > 0 ? 1u : first);
+            }
             mma_commit_w(smem_u32(&bars->o_full[t]));
             mma_commit_w(smem_u32(&bars->v_empty[vp.slot]));
             vp.next();
