@@ -433,18 +433,25 @@ __device__ __forceinline__ bool produce(const TreeParams& p, const Piece& pc, co
     if (step < n_prefix) {
       // only the pages that hold filled slots
       const int boxes = min(TILE, pc.len - step * TILE + box_rows - 1) >> box_lg;
-      if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
       const int y = p.page_steps > 1 ? (step - first * p.page_steps) * TILE : 0;
-      for (int i = 0; i < boxes; ++i) {
-        int page = __shfl_sync(0xffffffffu, tab0, (first + i) & 31);
-        const bool outside = page < 0 || page >= a.c.ix.num_pages;
-        if (outside) page = a.c.ix.num_pages;  // past the pool: the copy fills in zeros
-        if (lane == 0) {
-          if (outside) flag_index(a.c.status);
+      // the step's pages (at most 8, within one window: their number divides 32), one to a lane
+      int page = __shfl_sync(0xffffffffu, tab0, (first + lane) & 31);
+      const bool outside = lane < boxes && (page < 0 || page >= a.c.ix.num_pages);
+      if (outside) {
+        flag_index(a.c.status);
+        page = a.c.ix.num_pages;  // past the pool: the copy fills in zeros
+      }
+      int pg[TILE / 16];
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(dst + c * (TILE * 128) + i * box_rows * 128, pool, bar, c * 64, y, pc.hk, page);
-        }
+      for (int i = 0; i < TILE / 16; ++i) pg[i] = __shfl_sync(0xffffffffu, page, i);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, boxes * box_rows * D * 2);
+#pragma unroll
+        for (int i = 0; i < TILE / 16; ++i)
+          if (i < boxes)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(dst + c * (TILE * 128) + i * box_rows * 128, pool, bar, c * 64, y, pc.hk, pg[i]);
       }
     } else if (lane == 0) {
       if (a.k_new != nullptr) {
