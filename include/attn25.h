@@ -363,7 +363,8 @@ ATTN25_API int attn_fwd_fp8(const uint8_t* q8, const uint8_t* k8, const float* q
  * page per batch row (page_size = capacity) is a plain contiguous cache.
  *
  * D in {64, 128}.  page_size: 16, 32, 64, 128 or a multiple of 128.  A
- * row's capacity max_pages * page_size is at most 1048576 slots.  lens[b] is
+ * row's capacity max_pages * page_size is at most 1048576 slots; B * Hkv is
+ * at most 65535 and B * Hq at most 16777216.  lens[b] is
  * the number of filled slots; table entries behind the last page in use are
  * not read, and rows behind lens[b] may hold anything (NaN included).
  * page_table NULL: row b's pages are b * max_pages, b * max_pages + 1, ...

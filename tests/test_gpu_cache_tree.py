@@ -345,3 +345,11 @@ def test_refusals(ta):
             go(**bad)
     torch.cuda.synchronize()
     assert ta.attn_get_status() == 0
+
+
+def test_a_workspace_without_its_memory_is_refused(ta):
+    """An expanded view has the size but not the bytes."""
+    c = CacheCase(19, [5], 4, 2, 64, 16, 2)
+    ws = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(ta.attn_tree_workspace_size(4, 2, 2, 64))
+    with pytest.raises(ValueError):
+        call(ta, c, None, ws=ws)

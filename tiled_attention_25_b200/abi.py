@@ -608,6 +608,8 @@ def attn_tree_fwd(q, k_new, v_new, cache: AttnCache, out, lse, workspace, parent
     lse: fp32 [B][Hq][T] or None; parents: int32 [B][T]; counts: int32 [B]."""
     _, Hq, T, D = q.shape
     B, own = cache.B, cache._own
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     shape, kv_shape = (B, Hq, T, cache.D), (B, cache.Hkv, T, cache.D)
     (q_ptr, k_ptr, v_ptr, o_ptr), lay = cache._views(q=(q, shape), k=(k_new, kv_shape), v=(v_new, kv_shape), out=(out, shape))
     cache._call("attn_tree_fwd", LIB.attn_tree_fwd, stream, q_ptr, k_ptr, v_ptr, cache._ref, o_ptr,
