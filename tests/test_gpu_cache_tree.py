@@ -353,3 +353,24 @@ def test_a_workspace_without_its_memory_is_refused(ta):
     ws = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(ta.attn_tree_workspace_size(4, 2, 2, 64))
     with pytest.raises(ValueError):
         call(ta, c, None, ws=ws)
+
+
+@pytest.mark.parametrize("Hq,T", [(8, 1), (12, 5), (24, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_same_bits_whatever_ran_before(ta, D, Hq, T):
+    """Widely spread scores, so that running maxima move: when they do may not
+    depend on the tile's unused rows, where shared memory holds what an
+    earlier kernel left."""
+    lens = [900 + 7 * b for b in range(80)]  # more items than SMs: pieces of many steps
+    c = CacheCase(20, lens, Hq, 2, D, 64, T, scale=1.0)
+    before = CacheCase(21, [9000, 8000], 128, 1, D, 64, 1)  # queries in all 128 rows
+    o = [torch.empty_like(before.q_t), torch.empty(2, 128, 1, device="cuda")]
+    ws = [ta.new_tree_workspace(128, 1, 1, D), ta.new_tree_workspace(Hq, 2, T, D)]
+    first = None
+    for size in (0.0, 1.0, 30.0, -30.0):
+        before.q_t.mul_(0).add_(size)
+        out, lse = torch.empty_like(c.q_t), torch.empty(80, Hq, T, device="cuda")
+        call(ta, before, None, o[0], o[1], ws=ws[0])
+        call(ta, c, None, out, lse, ws=ws[1])  # the next kernel
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), size

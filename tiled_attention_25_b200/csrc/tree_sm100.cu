@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           if (!SOFTCAP) mx *= sl2;  // -inf stays -inf (sl2 > 0)
           const float m_new = fmaxf(m_run, mx);
-          const bool need = m_new > m_run + kTreeRescale;
+          const bool need = valid && m_new > m_run + kTreeRescale;  // (the other rows are not looked at: they hold anything)
           if (__any_sync(0xffffffffu, need)) {
             const float alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
             if (j > 1) {  // O must be complete before it is rescaled
