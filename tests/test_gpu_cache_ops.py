@@ -173,6 +173,26 @@ def test_weights_of_a_prompt_shared_by_clusters(ta, Hq, Hkv, lens, T):
     assert ta.attn_get_status() == 0
 
 
+@pytest.mark.parametrize("D,page", [(64, 64), (128, 16)])
+@pytest.mark.parametrize("path", [False, True])
+@pytest.mark.parametrize("B,T,Hq,Hkv", [(15, 28, 28, 4), (3, 70, 8, 2), (30, 40, 8, 1)])
+def test_weights_of_uneven_counts(ta, D, page, B, T, Hq, Hkv, path):
+    """More than one Q tile, few new tokens, long rows: many units to a CTA or to a
+    cluster, some with queries for its first CTA only."""
+    lens = [561 + 1031 * b // max(1, B - 1) for b in range(B)]
+    counts = [1 + (5 * b + T // 2) % T for b in range(B)]
+    c, p, lse, w = weights_case(B + T, lens, counts, T, Hq, Hkv, D, page, path)
+    check_weights(ta, c, p, lse, w)
+    outs = []
+    for _ in range(4):
+        out = torch.zeros(c.B, Hkv, c.cap, device="cuda")
+        ta.attn_cache_weights(c.q_t, torch.from_numpy(lse).cuda(), c.cache, None, out, path=i32(p), counts=i32(counts),
+                              scale=c.scale)
+        outs.append(out)
+    assert all(torch.equal(outs[0], x) for x in outs[1:])
+    assert ta.attn_get_status() == 0
+
+
 def test_weights_of_many_rows(ta):
     lens = [0, 1, 15, 16, 17, 127, 128, 129, 256, 257] * 4
     counts = [min(n, 2) for n in lens]

@@ -28,7 +28,7 @@ def roles(sim, units, kbufs, qslots, gathered=False):
         sim.bar(f"unit_full{i}", 1)
         sim.bar(f"unit_empty{i}", 7)
     for i in range(2):
-        sim.bar(f"j_full{i}", 1)
+        sim.bar(f"j_full{i}", 2)
         sim.bar(f"j_empty{i}", 1)
         for t in range(2):
             sim.bar(f"s_full{t}{i}", 1)
@@ -167,11 +167,10 @@ def roles(sim, units, kbufs, qslots, gathered=False):
                 if j < n - 1 or not keep:
                     sim.arrive(f"c_empty{(ql - 1) % COLS}")
             if t < tiles and n > 1:
-                if not owner:
-                    if joins and not (yield full(f"j_empty{t}", joins - 1)):
-                        return
-                    sim.arrive(f"j_full{t}")
-                else:
+                if joins and not (yield full(f"j_empty{t}", joins - 1)):
+                    return
+                sim.arrive(f"j_full{t}")
+                if owner:
                     if not (yield full(f"j_full{t}", joins)):
                         return
                     sim.arrive(f"j_empty{t}")
@@ -210,3 +209,60 @@ def test_a_wait_that_runs_out_ends_every_role(role):
                 stuck = sim.run(roles(sim, UNITS[name], (2, 2), 2), give_up=(role, at))
                 assert stuck is None, f"{role} wait {at}, seed {seed}: {stuck}"
                 assert sim.in_flight_at_exit == 0, f"{role} wait {at}, seed {seed}: {sim.pending_at_exit}"
+
+
+def joins_of_a_key_tile(sim, units, ctas, warps=2):
+    """The sums' barriers alone, warp by warp: two warpgroups to each CTA of a
+    cluster, any speed of each warp.  units: the steps of each CTA."""
+    for c in range(ctas):
+        sim.bar(f"j_full{c}", 2 * warps)
+        sim.bar(f"j_empty{c}", warps)
+        sim.bar(f"x_empty{c}", 2 * warps)
+    sim.bar("x_full", (ctas - 1) * 2 * warps)
+    joined, handed = {}, {}  # what lies in the buffers, and who has read it
+
+    def warp(c, sb, w):
+        sc = joins = 0
+        for it, steps in enumerate(units):
+            n = steps[c]
+            owner = (sc + max(n, 1) - 1) % 2 == sb
+            sc += n
+            if n > 1:
+                if joins and not (yield sim.full(f"j_empty{c}", joins - 1)):
+                    return
+                if not owner:
+                    joined[c, w] = it
+                sim.arrive(f"j_full{c}")
+                if owner:
+                    if not (yield sim.full(f"j_full{c}", joins)):
+                        return
+                    assert joined[c, w] == it
+                    sim.arrive(f"j_empty{c}")
+                joins += 1
+            if ctas > 1 and c > 0:
+                if it and not (yield sim.full(f"x_empty{c}", it - 1)):
+                    return
+                if owner:
+                    handed[c, w] = it
+                sim.arrive("x_full")
+            elif ctas > 1:
+                if not (yield sim.full("x_full", it)):
+                    return
+                if owner:
+                    assert all(handed[x, w] == it for x in range(1, ctas))
+                for x in range(1, ctas):
+                    sim.arrive(f"x_empty{x}")
+
+    return {f"cta{c} sums{sb} warp{w}": warp(c, sb, w) for c in range(ctas) for sb in range(2) for w in range(warps)}
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 4])
+@pytest.mark.parametrize("most", [1, 2, 3, 5])
+def test_sums_meet_once_a_unit(ctas, most):
+    """Units of many and of few steps, and of none for some CTAs: no warp takes
+    one phase of the sums' barriers for another, or reads another unit's sum."""
+    for seed in range(250):
+        sim = Sim(seed)
+        units = [[sim.rng.randint(0 if c else 1, most) for c in range(ctas)] for _ in range(6)]
+        stuck = sim.run(joins_of_a_key_tile(sim, units, ctas))
+        assert stuck is None, f"seed {seed}, {units}: {stuck}"

@@ -86,8 +86,9 @@ struct WBarriers {
   // own, since the sums keep them for longer than the products keep Q.
   uint64_t c_full[kColSlots], c_empty[kColSlots];
   uint64_t s_full[2][2], s_empty[2][2];
-  uint64_t j_full[2], j_empty[2];  // the other warpgroup's sum of a key tile: written; read
-  uint64_t x_full[2], x_empty[2];  // a cluster's sums: written by the others (first CTA); read (the others)
+  uint64_t j_full[2], j_empty[2];  // the other warpgroup's sum of a key tile: written (all 8 warps); read (4)
+  uint64_t x_full[2], x_empty[2];  // a cluster's sums: written by the others (first CTA, all their threads of the
+                                   // key tile); read (the others, 8 warps)
   uint64_t drain;
   uint32_t tmem_base, abort_flag, never_set;
   Unit unit[kUnits];
@@ -369,10 +370,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(smem_u32(&bars->unit_empty[i]), kUnitReaders);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->j_full[i]), 4);
+      mbar_init(smem_u32(&bars->j_full[i]), 8);
       mbar_init(smem_u32(&bars->j_empty[i]), 4);
-      mbar_init(smem_u32(&bars->x_full[i]), max(1, (p.split - 1) * TILE));  // (unused where split is 1)
-      mbar_init(smem_u32(&bars->x_empty[i]), 4);
+      mbar_init(smem_u32(&bars->x_full[i]), max(1, (p.split - 1) * 2 * TILE));  // (unused where split is 1)
+      mbar_init(smem_u32(&bars->x_empty[i]), 8);
       for (int t = 0; t < 2; ++t) {
         mbar_init(smem_u32(&bars->s_full[t][i]), 1);
         mbar_init(smem_u32(&bars->s_empty[t][i]), 4);
@@ -753,13 +754,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (lane == 0 && (j < u.n_rt - 1 || !u.keep_q)) mbar_arrive(smem_u32(&bars->c_empty[slot]));
       }
       if (!ok) break;
+      // A barrier's parity tells a phase only from its neighbours.  So that no warp
+      // can run ahead of a phase, or fall behind one, every warp of the key tile has a
+      // part in each: it waits for the phase before, and the next needs its arrival.
       if (here && u.n_rt > 1) {  // both warpgroups had steps
-        if (!owner) {
-          if (joins > 0 && !w_wait(smem_u32(&bars->j_empty[t]), (joins - 1) & 1, wc)) break;
-          x_buf[r] = total;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->j_full[t]));
-        } else {
+        if (joins > 0 && !w_wait(smem_u32(&bars->j_empty[t]), (joins - 1) & 1, wc)) break;
+        if (!owner) x_buf[r] = total;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->j_full[t]));
+        if (owner) {
           if (!w_wait(smem_u32(&bars->j_full[t]), joins & 1, wc)) break;
           total += x_buf[r];
           __syncwarp();
@@ -768,13 +771,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ++joins;
       }
       if (p.split > 1) {
-        if (owner && rank > 0) {  // hand the sum to the first CTA once it has read the last unit's
+        if (rank > 0) {  // hand the sum to the first CTA once it has read the last unit's
           if (shared > 0 && !wait_cluster(smem_u32(&bars->x_empty[t]), (shared - 1) & 1, wc)) break;
-          st_cluster(in_cta(smem_u32(x_buf + rank * TILE + r), 0), total);
+          if (owner) st_cluster(in_cta(smem_u32(x_buf + rank * TILE + r), 0), total);
           arrive_cluster(in_cta(smem_u32(&bars->x_full[t]), 0));
-        } else if (owner) {
+        } else {
           if (!wait_cluster(smem_u32(&bars->x_full[t]), shared & 1, wc)) break;
-          for (int x = 1; x < p.split; ++x) total += x_buf[x * TILE + r];
+          if (owner)
+            for (int x = 1; x < p.split; ++x) total += x_buf[x * TILE + r];
           __syncwarp();
           if (lane > 0 && lane < p.split) arrive_cluster(in_cta(smem_u32(&bars->x_empty[t]), lane));
         }
