@@ -382,10 +382,10 @@ __device__ __forceinline__ uint4 ancestor_bits(const TreeArgs& a, int b, int t, 
   const int32_t* par = a.parents + static_cast<long long>(b) * a.T;
   uint4 w = make_uint4(0u, 0u, 0u, 0u);
   bool bad = false;
-  for (int x = t; x >= 0;) {
+  for (int x = t; x >= x0;) {  // (ancestors only get smaller)
     const int i = x - x0;
     const uint32_t bit = 1u << (i & 31);
-    if (i >= 0 && i < 32) w.x |= bit;
+    if (i < 32) w.x |= bit;
     if (i >= 32 && i < 64) w.y |= bit;
     if (i >= 64 && i < 96) w.z |= bit;
     if (i >= 96 && i < 128) w.w |= bit;
