@@ -143,4 +143,38 @@ ATTN25_HD int slot_from_begin(int first_cut) { return 2 * first_cut - 1; }
 // its first inner cut, or of its first piece), lie at the head of the workspace.
 constexpr int kTreeCounterBytes = 1024;
 
+// --------------------------------------------------------------- eviction plan
+//
+// Shared memory of one CTA of a plan, of kPlanSmem bytes at most: `fixed` bytes
+// of counters, then the ranks of `held` slots (4 bytes each), then a flag byte
+// to four of its `share` of the slots.  The flags are always there; the ranks of
+// a share that does not fit beside them are formed again from global memory.
+constexpr int kPlanSmem = 227 * 1024;
+constexpr int kPlanMaxCtas = 8;  // CTAs of a cluster, which share a head
+constexpr int kPlanThreads = 1024;
+
+struct PlanLayout {
+  int ctas, share, held, kept, bytes;  // kept: offset of the flags
+};
+
+ATTN25_HD int plan_share(int slots, int ctas) { return ((slots + ctas - 1) / ctas + 31) / 32 * 32; }
+
+// CTAs to a head: as many as it takes for a share's flags to fit (two above
+// about 796 thousand slots); more while one to an SM is not exceeded and each
+// keeps a quad for every thread.
+ATTN25_HD PlanLayout plan_layout(int heads, int capacity, int sms, int fixed) {
+  PlanLayout p;
+  p.ctas = 1;
+  while (p.ctas < kPlanMaxCtas &&
+         (fixed + plan_share(capacity, p.ctas) / 4 > kPlanSmem ||
+          (heads * p.ctas * 2 <= sms && capacity / (p.ctas * 2) >= 4 * kPlanThreads)))
+    p.ctas *= 2;
+  p.share = plan_share(capacity, p.ctas);
+  const int room = (kPlanSmem - fixed - p.share / 4) / 16 * 4;
+  p.held = p.share < room ? p.share : room;
+  p.kept = fixed + p.held * 4;
+  p.bytes = p.kept + p.share / 4;
+  return p;
+}
+
 }  // namespace attn25

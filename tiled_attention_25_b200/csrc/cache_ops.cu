@@ -165,10 +165,8 @@ __device__ __forceinline__ uint32_t slot_rank(float w, int pos, int first, int r
 // over the lanes, the warps and the CTAs.  A walk's cost is its latency, so a
 // lane takes four neighbouring slots at a time (one 16-byte access): halving 32
 // heads of up to 65000 slots took 34 us with one slot to a lane.
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kPlanSmem = 227 * 1024;
 
 struct alignas(16) PlanShared {
   int hist[kBins];      // this CTA's, of the current pass
@@ -179,6 +177,8 @@ struct alignas(16) PlanShared {
   uint32_t digit;
   int need, in_bin;
 };
+// the longest row's flags fit beside the counters
+static_assert(sizeof(PlanShared) + kMaxCapacity / kPlanMaxCtas / 4 <= kPlanSmem, "flags of a share");
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
     const int32_t* pos = a.positions + static_cast<long long>(bh) * a.ix.capacity;
     const int recent_from = static_cast<int>(max(static_cast<long long>(a.seen[b]) - a.recent, static_cast<long long>(INT_MIN)));
     // this CTA's slots [j0, j0 + m) in quads of four
-    const int share = ((n + ctas - 1) / ctas + 31) / 32 * 32;
+    const int share = plan_share(n, ctas);
     const int j0 = min(n, rank * share), m = min(n - j0, share), quads = (m + 3) / 4;
     const bool held = share <= a.held_keys;
     auto fresh = [&](int q) {
@@ -488,25 +488,21 @@ cudaError_t launch_cache_compact(const CompactArgs& a, int sms, cudaStream_t str
 cudaError_t launch_evict_plan(const PlanArgs& args, int sms, cudaStream_t stream) {
   PlanArgs a = args;
   const int heads = a.ix.B * a.ix.Hkv;
-  // CTAs to a head: more while one to an SM is not exceeded and each keeps a quad for every thread
-  int ctas = 1;
-  while (ctas < 8 && heads * ctas * 2 <= sms && a.ix.capacity / (ctas * 2) >= 4 * kPlanThreads) ctas *= 2;
-  const int share = ((a.ix.capacity + ctas - 1) / ctas + 31) / 32 * 32;
-  const int room = (kPlanSmem - static_cast<int>(sizeof(PlanShared)) - share / 4) / 16 * 4;
-  a.held_keys = share < room ? share : room;  // a row shorter than the capacity has a smaller share
+  // a row shorter than the capacity has a smaller share
+  const PlanLayout lay = plan_layout(heads, a.ix.capacity, sms, static_cast<int>(sizeof(PlanShared)));
+  a.held_keys = lay.held;
   a.aligned = ((reinterpret_cast<uintptr_t>(a.weights) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
-  const size_t smem = sizeof(PlanShared) + static_cast<size_t>(a.held_keys) * 4 + share / 4;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = prepare_kernel(done, plan_kernel, kPlanSmem, 0);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(heads * ctas);
+  cfg.gridDim = dim3(heads * lay.ctas);
   cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = lay.bytes;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.x = lay.ctas;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
