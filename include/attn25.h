@@ -423,7 +423,8 @@ ATTN25_API int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new
  * row with no filled slot then gets O = 0 and LSE = -inf.  Rows t >=
  * counts[b] of out and lse are left as they were, and such rows of q, k_new
  * and v_new may hold anything.  (As in attn_fwd, an infinite or NaN value of
- * a real token reaches the rows of its tile that do not see it.)  A parent
+ * a real token reaches the rows of its tile that do not see it.)  A query with
+ * a visible score of NaN or +infinity gets O = LSE = NaN.  A parent
  * outside [-1, t) counts as -1 (ATTN_ERR_INDEX).
  * mod_kind: ATTN_MOD_NONE or ATTN_MOD_SOFTCAP (slots of a cache that has
  * evicted some have no index to mask by; ATTN_ERR_UNSUPPORTED otherwise).

@@ -4,9 +4,10 @@ import pytest
 import torch
 
 import oracle
-from cache_common import i32
+from cache_common import CacheCase, check_tree, i32
 
 pytestmark = pytest.mark.gpu
+NAN = float("nan")
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +47,43 @@ def test_plan_of_long_tables_and_many_heads(ta, cap, page, lens):
                                            first, recent)
         assert int(count[b, 0]) == wn[0, 0], (b, n)
         assert np.array_equal(moves[b].cpu().numpy(), want[0]), (b, n)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq", [(1, 4), (9, 8), (40, 4)])
+def test_scores_that_are_not_finite(ta, D, T, Hq):
+    """A visible key whose score is NaN or +inf leaves a row without a softmax:
+    O and LSE are NaN.  A score of -inf is a weight of zero."""
+    lens = [300, 128, 20000, 5]  # whole items, and one cut into pieces
+    c = CacheCase(T + D, lens, Hq, 2, D, 128, T)
+    ws = ta.new_tree_workspace(Hq, 2, T, D)
+
+    def call():
+        out, lse = torch.empty_like(c.q_t), torch.empty(4, Hq, T, device="cuda")
+        ta.attn_tree_fwd(c.q_t, c.k_new_t, c.v_new_t, c.cache, out, lse, ws, scale=c.scale)
+        torch.cuda.synchronize()
+        return out, lse
+
+    place = lambda b, slot: (int(c.table[b, slot // 128]), 0, slot % 128)  # head 0
+    good_out, good_lse = call()
+    for b, slot in ((0, 17), (2, 11111), (3, 4)):
+        c.k_t[place(b, slot)] = NAN
+    out, lse = call()
+    hit = torch.zeros(4, Hq, T, dtype=torch.bool, device="cuda")
+    hit[[0, 2, 3], : Hq // 2] = True
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    assert torch.equal(lse[~hit], good_lse[~hit]) and torch.equal(out[~hit], good_out[~hit])
+    for b, slot in ((0, 17), (2, 11111), (3, 4)):
+        c.k_t[place(b, slot)] = 0.0
+        c.k[place(b, slot)] = 0.0
+        c.k_t[place(b, slot)][3] = float("inf")
+        c.k[place(b, slot)][3] = np.inf
+    out, lse = call()
+    hit &= c.q_t[..., 3] > 0
+    assert hit.any() and not hit[:, : Hq // 2].all()
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    want = oracle.cache.tree_attention(c.q, c.k_new, c.v_new, c.k, c.v, c.table, c.lens, None, None, c.scale)
+    for x in want:
+        x[hit.cpu().numpy()] = np.nan  # no definition
+    check_tree(out, lse, want)
+    assert ta.attn_get_status() == 0

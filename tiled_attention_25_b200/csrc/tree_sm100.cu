@@ -318,6 +318,11 @@ __device__ __forceinline__ bool walk_next(Walk& w, const TreeParams& p, int grou
   return true;
 }
 
+// ln of a row's sum l 2^m: -inf without a visible key, NaN where a score was NaN
+// or +inf (l is NaN then; it adds to the slots' totals, and must not look like an
+// empty row).
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * LN2; }
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -563,8 +568,7 @@ __device__ __forceinline__ void join_rows(const TreeParams& p, const Piece& pc, 
 #pragma unroll
       for (int d = 0; d < kCols; d += 2) orow[lane * (kCols / 2) + d / 2] = pack_bf16x2(o[y][d] * inv, o[y][d + 1] * inv);
       if (lane == 0 && a.lse != nullptr)
-        a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] =
-            l[y] > 0.f ? (m[y] + log2f(l[y])) * LN2 : -INFINITY;
+        a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] = row_lse(m[y], l[y]);
     }
   }
 }
@@ -917,8 +921,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (valid && t == 0 && copy == 0) {
         if (pc.slot >= 0) p.part_ml[part + r] = make_float2(m, l);
         else if (a.lse != nullptr)
-          a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] =
-              l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+          a.lse[(static_cast<long long>(pc.b) * a.Hq + pc.hk * a.G + head) * a.T + tok] = row_lse(m, l);
       }
       // where this thread writes: rows w_row + 32 x, four columns
       const int w_row = (warp & 3) * 8 + (lane >> 2), quad = lane & 3;
