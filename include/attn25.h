@@ -400,7 +400,9 @@ typedef struct attn_cache {
  * lens_out[b] = lens[b] + counts[b]; NULL: the cache's lens are advanced in
  * place (one more small launch, since every block reads them first).
  * Tokens beyond the capacity and path entries outside [0, T) are not
- * written (ATTN_ERR_INDEX); the length stops at the capacity.
+ * written, K, V or position (ATTN_ERR_INDEX); the length stops at the
+ * capacity.  A token whose slot lies in a page outside the pool has its
+ * position written all the same: the slot is its own, and reads as zeros.
  */
 ATTN25_API int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new, const attn_bf16* v_new,
                                  int32_t* lens_out, const int32_t* path, const int32_t* counts, int T,
@@ -489,8 +491,9 @@ ATTN25_API int attn_evict_plan(const attn_cache* cache, const float* weights, co
  * particular order, which attention does not mind; positions keep their
  * places.  moves may come from attn_evict_plan or be the caller's own
  * (any policy): within a (row, head) the `to` slots must be distinct and no
- * slot both read and written.  A move outside [0, capacity) is left out
- * (ATTN_ERR_INDEX).
+ * slot both read and written.  A move outside [0, capacity), or one of whose
+ * slots lies in a page outside the pool, is left out whole, weight and position
+ * with the row (ATTN_ERR_INDEX).
  */
 ATTN25_API int attn_cache_compact(const attn_cache* cache, const int32_t* moves, const int32_t* n_moves,
                                   int budget, float* weights, int32_t* positions, attn_stream_t stream);

@@ -87,3 +87,28 @@ def test_scores_that_are_not_finite(ta, D, T, Hq):
         x[hit.cpu().numpy()] = np.nan  # no definition
     check_tree(out, lse, want)
     assert ta.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+@pytest.mark.parametrize("storage", ["head", "row"])
+def test_moves_from_and_into_a_page_outside_the_pool(ta, bad, storage):
+    """Such a move is left out whole: weight and position stay with the row's
+    K and V."""
+    c = CacheCase(5, [256, 200], 2, 2, 64, 64, storage=storage)
+    c.table[0, 3] = c.table[1, 0] = bad
+    c.load()
+    w = c.rng.exponential(size=(2, 2, c.cap)).astype(np.float32)
+    pos = np.tile(np.arange(c.cap), (2, 2, 1))
+    moves = np.array([[[5, 200], [6, 130], [70, 191]], [[5, 130], [66, 150], [7, 199]]], dtype=np.int32)
+    moves = np.repeat(moves[:, None], 2, axis=1)  # row 0 reads the bad page once, row 1 writes it twice
+    w_t, pos_t = torch.from_numpy(w).cuda(), i32(pos)
+    ta.attn_cache_compact(c.cache, i32(moves), i32(np.full((2, 2), 3)), 3, weights=w_t, positions=pos_t)
+    torch.cuda.synchronize()
+    assert ta.attn_get_status() == ta.ATTN_ERR_INDEX
+    done = np.full((2, 2, 3, 2), -1)
+    done[0, :, :2], done[1, :, :1] = moves[0, :, 1:], moves[1, :, 1:2]
+    new = oracle.cache.compact(done, np.array([[2, 2], [1, 1]]), 3, c.k, c.v, c.table, c.lens, w, pos)
+    assert np.array_equal(c.k_t.float().cpu().double().numpy(), c.k, equal_nan=True)
+    assert np.array_equal(c.v_t.float().cpu().double().numpy(), c.v, equal_nan=True)
+    assert np.array_equal(w_t.cpu().numpy(), w) and np.array_equal(pos_t.cpu().numpy(), pos)
+    assert np.array_equal(c.lens_t.cpu().numpy(), new)

@@ -119,10 +119,12 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const CompactArgs
         const int2 mv = moves[i];
         if (mv.x >= 0 && mv.x < a.c.ix.capacity && mv.y >= 0 && mv.y < a.c.ix.capacity) {
           const long long to = slot_entry(a.c.ix, b, hk, mv.x), from = slot_entry(a.c.ix, b, hk, mv.y);
-          if (a.weights != nullptr) a.weights[to] = a.weights[from];
-          if (a.positions != nullptr) a.positions[to] = a.positions[from];
+          const float weight = a.weights != nullptr ? a.weights[from] : 0.f;
+          const int32_t position = a.positions != nullptr ? a.positions[from] : 0;
           const int pt = page_at(a.c.ix, b, mv.x / ps), pf = page_at(a.c.ix, b, mv.y / ps);
-          if (pt >= 0 && pf >= 0) {
+          if (pt >= 0 && pf >= 0) {  // weight and position go with the row, or stay with it
+            if (a.weights != nullptr) a.weights[to] = weight;
+            if (a.positions != nullptr) a.positions[to] = position;
             moved = true;
             t.dst[0][threadIdx.x] = pt * a.c.k_st.b + mv.x % ps * a.c.k_st.s;
             t.dst[1][threadIdx.x] = pt * a.c.v_st.b + mv.x % ps * a.c.v_st.s;
