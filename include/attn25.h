@@ -398,7 +398,9 @@ typedef struct attn_cache {
  * positions (device int32 [B][Hkv][capacity], or NULL): the new slots get
  * seen[b] + i (seen NULL: lens[b] + i), each token's place in the sequence.
  * lens_out[b] = lens[b] + counts[b]; NULL: the cache's lens are advanced in
- * place (one more small launch, since every block reads them first).
+ * place.  lens_out may be lens, counts or seen (in place: one more small
+ * launch, since every block reads them first), but not overlap them otherwise
+ * (ATTN_ERR_ARG).
  * Tokens beyond the capacity and path entries outside [0, T) are not
  * written, K, V or position (ATTN_ERR_INDEX); the length stops at the
  * capacity.  A token whose slot lies in a page outside the pool has its

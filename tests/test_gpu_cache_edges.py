@@ -112,3 +112,23 @@ def test_moves_from_and_into_a_page_outside_the_pool(ta, bad, storage):
     assert np.array_equal(c.v_t.float().cpu().double().numpy(), c.v, equal_nan=True)
     assert np.array_equal(w_t.cpu().numpy(), w) and np.array_equal(pos_t.cpu().numpy(), pos)
     assert np.array_equal(c.lens_t.cpu().numpy(), new)
+
+
+@pytest.mark.parametrize("which", ["seen", "counts", "lens"])
+def test_new_lengths_in_the_place_of_an_argument(ta, which):
+    """lens_out may be an array that the call reads: every block has read it by then."""
+    B, T = 6, 900
+    counts = np.array([T, 0, 13, 500, 1, T])
+    c = CacheCase(6, [0, 30, 129, 7, 64, 1], 2, 2, 64, 64, T, room=T)
+    seen = c.lens + 1000
+    args = {"seen": i32(seen), "counts": i32(counts), "lens": c.lens_t}
+    pos = np.full((B, 2, c.cap), -1)
+    pos_t = i32(pos)
+    ta.attn_cache_append(c.cache, c.k_new_t, c.v_new_t, args[which], counts=args["counts"], positions=pos_t, seen=args["seen"])
+    want = oracle.cache.append(c.k_new, c.v_new, c.k, c.v, c.table, c.lens, None, counts, pos, seen)
+    torch.cuda.synchronize()
+    assert ta.attn_get_status() == 0
+    assert np.array_equal(c.k_t.float().cpu().double().numpy(), c.k, equal_nan=True)
+    assert np.array_equal(pos_t.cpu().numpy(), pos)
+    for name, before in (("seen", seen), ("counts", counts), ("lens", c.lens)):
+        assert np.array_equal(args[name].cpu().numpy(), want if name == which else before), name

@@ -51,8 +51,8 @@ struct AppendArgs {
   const int32_t* counts;
   const int32_t* seen;
   int32_t* positions;
-  int32_t* lens;      // the cache's own lens (advanced in place when lens_out is nullptr)
   int32_t* lens_out;
+  bool late;  // lens_out is one of the arrays read here: written by a launch of its own
   int T;
 };
 

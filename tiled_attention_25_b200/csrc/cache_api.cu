@@ -2,6 +2,7 @@
 // function is declared in include/attn25.h.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -79,6 +80,12 @@ bool encode_pool(CUtensorMap* m, const void* pool, const attn_cache* c, const St
   return encode_bf16_4d(m, pool, c->D, c->page_size, c->Hkv, c->num_pages, st, c->page_size < TILE ? c->page_size : TILE);
 }
 
+// Do two int32 arrays of n entries share memory?
+bool rows_meet(const int32_t* x, const int32_t* y, int n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return (a < b ? b - a : a - b) < static_cast<uintptr_t>(n) * sizeof(int32_t);
+}
+
 int launched(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH; }
 
 }  // namespace
@@ -99,6 +106,12 @@ int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new, const att
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(lens_out) || !aligned4(path) || !aligned4(counts) ||
       !aligned4(positions) || !aligned4(seen))
     return ATTN_ERR_ALIGN;
+  if (lens_out == nullptr) lens_out = cache->lens;
+  bool late = false;
+  for (const int32_t* read : {static_cast<const int32_t*>(cache->lens), counts, seen}) {
+    late = late || lens_out == read;
+    if (read != nullptr && lens_out != read && rows_meet(lens_out, read, cache->B)) return ATTN_ERR_ARG;
+  }
   AppendArgs a{};
   if (!layout_of(layouts ? &layouts->k : nullptr, cache->Hkv, T, cache->D, a.kn_st) ||
       !layout_of(layouts ? &layouts->v : nullptr, cache->Hkv, T, cache->D, a.vn_st))
@@ -113,8 +126,8 @@ int attn_cache_append(const attn_cache* cache, const attn_bf16* k_new, const att
   a.counts = counts;
   a.seen = seen;
   a.positions = positions;
-  a.lens = cache->lens;
-  a.lens_out = lens_out == cache->lens ? nullptr : lens_out;
+  a.lens_out = lens_out;
+  a.late = late;
   a.T = T;
   return launched(launch_cache_append(a, d->sms, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -87,19 +87,20 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(const AppendArgs a
                  a.c.v + hk * a.c.v_st.h);
     __syncthreads();
   }
-  if (a.lens_out != nullptr && blockIdx.x == 0 && hk == 0 && threadIdx.x == 0)
+  if (!a.late && blockIdx.x == 0 && hk == 0 && threadIdx.x == 0)
     a.lens_out[b] = min(len + n, a.c.ix.capacity);
   if (bad) flag_index(a.c.status);
 }
 
-// The in-place advance of lens, after every block of append_kernel has read them.
+// The new lengths where they replace an array that the blocks of append_kernel
+// read, after all of them.
 __global__ void advance_kernel(const AppendArgs a) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= a.c.ix.B) return;
   bool bad = false;
   const int n = a.counts != nullptr ? clamp_count(a.counts[b], a.T, bad) : a.T;
-  const int len = clamp_count(a.lens[b], a.c.ix.capacity, bad);
-  a.lens[b] = min(len + n, a.c.ix.capacity);
+  const int len = clamp_count(a.c.ix.lens[b], a.c.ix.capacity, bad);
+  a.lens_out[b] = min(len + n, a.c.ix.capacity);
 }
 
 template <int D>
@@ -474,7 +475,7 @@ cudaError_t launch_cache_append(const AppendArgs& a, int sms, cudaStream_t strea
   if (a.c.D == 128) append_kernel<128><<<grid, kCopyThreads, 0, stream>>>(a);
   else append_kernel<64><<<grid, kCopyThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.lens_out != nullptr) return e;
+  if (e != cudaSuccess || !a.late) return e;
   advance_kernel<<<(a.c.ix.B + 255) / 256, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
