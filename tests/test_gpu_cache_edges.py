@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import oracle
-from cache_common import CacheCase, check_tree, i32
+from cache_common import CacheCase, check_tree, i32, random_tree, tree_reference
+from test_gpu_cache_ops import check_weights, weights_case
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -132,3 +133,129 @@ def test_new_lengths_in_the_place_of_an_argument(ta, which):
     assert np.array_equal(pos_t.cpu().numpy(), pos)
     for name, before in (("seen", seen), ("counts", counts), ("lens", c.lens)):
         assert np.array_equal(args[name].cpu().numpy(), want if name == which else before), name
+
+
+# ------------------------------------------------------------------ every form of the kernels
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,T", [(6, 3), (10, 10), (40, 4), (4, 130)])
+@pytest.mark.parametrize("softcap", [None, 2.0])
+def test_tree_of_any_number_of_query_rows(ta, D, Hq, T, softcap):
+    """9, 50 and 80 rows to a tile, and several tiles, with and without softcap:
+    whole items, and some cut into pieces."""
+    lens = [300, 5000, 0, 129]
+    c = CacheCase(Hq + T, lens, Hq, 2, D, 64, T, counts=[T, T, (T + 1) // 2, 1])
+    parents = random_tree(c.rng, 4, T)
+    kw = dict(mod_kind=ta.MOD_SOFTCAP, mod_params=ta.ModParams(softcap=softcap)) if softcap else {}
+    out, lse = torch.zeros_like(c.q_t), torch.zeros(4, Hq, T, device="cuda")
+    ta.attn_tree_fwd(c.q_t, c.k_new_t, c.v_new_t, c.cache, out, lse, ta.new_tree_workspace(Hq, 2, T, D), parents=i32(parents),
+                     counts=i32(c.counts), scale=c.scale, **kw)
+    torch.cuda.synchronize()
+    assert ta.attn_get_status() == 0
+    check_tree(out, lse, tree_reference(c, parents, softcap=softcap), f"{Hq} heads, {T} tokens")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,counts,T,Hq,Hkv,path", [
+    ([700, 300, 17], [9, 1, 4], 9, 6, 2, True),       # one Q tile of 27 rows, two slots to hold it
+    ([600, 129], [11, 12], 12, 16, 2, True),          # one Q tile of 96 rows
+    ([900, 257, 640], [70, 3, 41], 70, 8, 2, True),   # gathered tiles that stream
+    ([700, 257], None, 257, 4, 2, False),             # tiles that stream, shared by clusters
+    ([1500], None, 1100, 8, 1, False),
+])
+def test_weights_with_softcap(ta, D, lens, counts, T, Hq, Hkv, path):
+    c, p, lse, w = weights_case(T + D, lens, counts, T, Hq, Hkv, D, 64, path, softcap=2.0)
+    check_weights(ta, c, p, lse, w, softcap=2.0)
+    assert ta.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_of_one_token_and_many_long_rows(ta, D):
+    """A plain decode loop's call, without a path."""
+    lens = [4000 + 37 * b for b in range(24)]
+    c, p, lse, w = weights_case(D, lens, None, 1, 8, 2, D, 128, False)
+    check_weights(ta, c, p, lse, w, inplace=True)
+    assert ta.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("path", [False, True])
+def test_weights_of_many_rows_and_query_tiles(ta, path):
+    """More rows than a warp looks at together, more than one Q tile to a row."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(40, 900, 70)
+    counts = rng.integers(0, 41, 70)
+    c, p, lse, w = weights_case(3, lens, counts, 40, 8, 2, 64, 64, path)
+    check_weights(ta, c, p, lse, w)
+    assert ta.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,n", [(300, 2000), (130, 0)])
+def test_chunks_of_a_prompt(ta, D, T, n):
+    """A chunk over a filled cache: attention as a chain, its rows appended, its
+    weights; each of its queries spreads a weight of one."""
+    Hq, Hkv, page = 8, 2, 128
+    c = CacheCase(T, [n, n // 3], Hq, Hkv, D, page, T, room=T)
+    out, lse = torch.zeros_like(c.q_t), torch.zeros(2, Hq, T, device="cuda")
+    ta.attn_tree_fwd(c.q_t, c.k_new_t, c.v_new_t, c.cache, out, lse, ta.new_tree_workspace(Hq, Hkv, T, D), scale=c.scale)
+    ta.attn_cache_append(c.cache, c.k_new_t, c.v_new_t)
+    w = torch.rand(2, Hkv, c.cap, device="cuda")
+    base = w.clone()
+    ta.attn_cache_weights(c.q_t, lse, c.cache, w, w, scale=c.scale)
+    torch.cuda.synchronize()
+    assert ta.attn_get_status() == 0
+    check_tree(out, lse, tree_reference(c, None))
+    lens = oracle.cache.append(c.k_new, c.v_new, c.k, c.v, c.table, c.lens, None, None)
+    want, add = oracle.cache.slot_weights(c.q, lse.cpu().double().numpy(), c.k, c.table, lens, base.double().cpu().numpy(), None,
+                                          None, c.scale)
+    got, live = w.cpu().double().numpy(), ~np.isnan(want)
+    # each exponential to 1e-4 relative (scores up to ~8 in fp32), the sum and the base rounded in fp32
+    assert (np.abs(got - want) <= 1e-4 * add + 1e-6 * np.abs(want))[live].all()
+    for b in range(2):
+        old = int(c.lens[b])
+        mass = got[b, :, : int(lens[b])].sum(-1) - base[b, :, :old].double().sum(-1).cpu().numpy()
+        # the weights of the tree's own LSE: 1e-4 each of the LSE and of the exponentials; fp32 totals
+        assert np.abs(mass - Hq // Hkv * T).max() <= 2e-4 * (Hq // Hkv) * T + 1e-6 * want[b][:, : int(lens[b])].sum()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,page", [(128, 8, 2, 64), (64, 6, 6, 16)])
+def test_an_accepted_path_spreads_a_weight_of_one(ta, D, Hq, Hkv, page):
+    """Rounds of drafting, accepting and evicting: the tree's LSE of an accepted
+    node is over just the slots that its weights go to, so each accepted query
+    adds one per head."""
+    B, T, budget, G = 3, 7, 90, Hq // Hkv
+    cache = ta.new_attn_cache(B, Hkv, 128, D, page_size=page)
+    cap = cache.capacity
+    rng, g = np.random.default_rng(D), torch.Generator(device="cuda").manual_seed(D)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    w, pos = torch.zeros(B, Hkv, cap, device="cuda"), torch.zeros(B, Hkv, cap, dtype=torch.int32, device="cuda")
+    moves = torch.empty(B, Hkv, budget, 2, dtype=torch.int32, device="cuda")
+    n_moves, seen = torch.empty(B, Hkv, dtype=torch.int32, device="cuda"), i32([0] * B)
+    ws = ta.new_tree_workspace(Hq, Hkv, T, D)
+    for step in range(60):  # about two tokens each
+        q, k, v = rnd(B, Hq, T, D), rnd(B, Hkv, T, D), rnd(B, Hkv, T, D)
+        parents = random_tree(rng, B, T)
+        out, lse = torch.empty_like(q), torch.empty(B, Hq, T, device="cuda")
+        ta.attn_tree_fwd(q, k, v, cache, out, lse, ws, parents=i32(parents))
+        path, accepted = np.zeros((B, T), dtype=np.int32), np.zeros(B, dtype=np.int32)
+        for b in range(B):
+            node, up = int(rng.integers(0, T)), []
+            while node >= 0:
+                up.append(node)
+                node = int(parents[b, node])
+            accepted[b] = len(up)
+            path[b, : len(up)] = up[::-1]
+        acc_t, live = i32(accepted), torch.arange(cap, device="cuda")[None, :] < cache.lens[:, None]
+        before = torch.where(live[:, None], w, 0.0).double().sum(-1)
+        ta.attn_cache_append(cache, k, v, path=i32(path), counts=acc_t, positions=pos, seen=seen)
+        ta.attn_cache_weights(q, lse, cache, w, w, path=i32(path), counts=acc_t)
+        seen += acc_t
+        live = torch.arange(cap, device="cuda")[None, :] < cache.lens[:, None]
+        after = torch.where(live[:, None], w, 0.0).double().sum(-1)
+        # 1e-4 each of the LSE and of the exponentials; fp32 totals
+        want = G * acc_t.double()[:, None]
+        assert ((after - before - want).abs() <= 2e-4 * want + 1e-6 * after).all(), step
+        ta.attn_evict_plan(cache, w, pos, seen, moves, n_moves, budget, 1, 16)
+        ta.attn_cache_compact(cache, moves, n_moves, budget, weights=w, positions=pos)
+    assert torch.equal(cache.lens, seen.clamp(max=budget)) and (seen > budget).all() and ta.attn_get_status() == 0
