@@ -259,3 +259,73 @@ def test_an_accepted_path_spreads_a_weight_of_one(ta, D, Hq, Hkv, page):
         ta.attn_evict_plan(cache, w, pos, seen, moves, n_moves, budget, 1, 16)
         ta.attn_cache_compact(cache, moves, n_moves, budget, weights=w, positions=pos)
     assert torch.equal(cache.lens, seen.clamp(max=budget)) and (seen > budget).all() and ta.attn_get_status() == 0
+
+
+# ------------------------------------------------------------------ layouts and offsets
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("path", [False, True])
+@pytest.mark.parametrize("T,Hq", [(5, 4), (70, 8)])
+def test_weights_of_strided_views(ta, D, path, T, Hq):
+    """q as [B][T][H][D] storage with room between its rows, pools as [page][row][head][D]."""
+    c, p, lse, w = weights_case(T, [300, T + 40], [T, T - 3], T, Hq, 2, D, 32, path)
+    check_weights(ta, c, p, lse, w)
+    wide = torch.full((2, T, Hq, D + 24), NAN, dtype=torch.bfloat16, device="cuda")
+    wide[..., 8: 8 + D] = c.q_t.permute(0, 2, 1, 3)
+    c.q_t = wide[..., 8: 8 + D].permute(0, 2, 1, 3)
+    c.storage = "row"
+    c.load()
+    check_weights(ta, c, p, lse, w)
+    assert ta.attn_get_status() == 0
+
+
+def test_append_weights_and_compact_beyond_32_bit_offsets(ta):
+    """Pages that start past 2^32 elements of the pool."""
+    page, D, T = 128, 64, 5
+    stride = 1 << 31  # elements between pages: the third page starts at 2^32
+    flat = torch.empty(2 * stride + page * D, dtype=torch.bfloat16, device="cuda")
+    pool = flat.as_strided((3, 1, page, D), (stride, page * D, D, 1))
+    c = CacheCase(16, [300], 4, 1, D, page, T, spare=0, room=T)
+    pool.copy_(c.k_t)
+    c.k_t = pool
+    c.cache = ta.AttnCache(pool, c.v_t, c.lens_t, c.table_t)
+    ta.attn_cache_append(c.cache, c.k_new_t, c.v_new_t)
+    c.lens = oracle.cache.append(c.k_new, c.v_new, c.k, c.v, c.table, c.lens, None, None).astype(np.int32)
+    torch.cuda.synchronize()
+    assert np.array_equal(pool.float().cpu().double().numpy(), c.k, equal_nan=True)
+    lse = np.full((1, 4, T), 5.0, dtype=np.float32)
+    check_weights(ta, c, None, lse, np.ones((1, 1, c.cap), dtype=np.float32))
+    moves = np.array([[[[3, 290], [140, 301], [200, 10]]]], dtype=np.int32)
+    ta.attn_cache_compact(c.cache, i32(moves), i32([[3]]), 3)
+    oracle.cache.compact(moves, np.array([[3]]), 3, c.k, c.v, c.table, c.lens)
+    torch.cuda.synchronize()
+    assert np.array_equal(pool.float().cpu().double().numpy(), c.k, equal_nan=True)
+    assert np.array_equal(c.v_t.float().cpu().double().numpy(), c.v, equal_nan=True) and ta.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("budget", [128, 500])
+def test_a_budget_that_nothing_exceeds(ta, budget):
+    """At the capacity and above it: no moves, and the lengths stay."""
+    c = CacheCase(3, [128, 77], 2, 2, 64, 64)
+    w, pos = torch.rand(2, 2, c.cap, device="cuda"), torch.zeros(2, 2, c.cap, dtype=torch.int32, device="cuda")
+    moves, n = torch.full((2, 2, budget, 2), 9, dtype=torch.int32, device="cuda"), i32(np.full((2, 2), 9))
+    ta.attn_evict_plan(c.cache, w, pos, i32([128, 77]), moves, n, budget, 4, 20)
+    ta.attn_cache_compact(c.cache, moves, n, budget, weights=w, positions=pos)
+    torch.cuda.synchronize()
+    assert (moves == -1).all() and (n == 0).all() and c.lens_t.tolist() == [128, 77] and ta.attn_get_status() == 0
+    assert np.array_equal(c.k_t.float().cpu().double().numpy(), c.k, equal_nan=True)
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_tree_over_thousands_of_rows(ta, T):
+    rng = np.random.default_rng(T)
+    lens = rng.integers(0, 90, 2100)
+    lens[rng.random(2100) < 0.3] = 0
+    c = CacheCase(T, lens, 2, 1, 64, 32, T, counts=rng.integers(0, T + 1, 2100))
+    out, lse = torch.zeros_like(c.q_t), torch.zeros(2100, 2, T, device="cuda")
+    ta.attn_tree_fwd(c.q_t, c.k_new_t, c.v_new_t, c.cache, out, lse, ta.new_tree_workspace(2, 1, T, 64), counts=i32(c.counts),
+                     scale=c.scale)
+    torch.cuda.synchronize()
+    assert ta.attn_get_status() == 0
+    check_tree(out, lse, tree_reference(c, None))
