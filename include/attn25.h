@@ -461,6 +461,8 @@ ATTN25_API int attn_tree_fwd(const attn_bf16* q, const attn_bf16* k_new, const a
  *   weights_in, weights_out: fp32 [B][Hkv][capacity], which may be the same
  *   array; entries behind lens[b] are left as they were.  1 <= T <= 262144.
  * Sums are formed in fp32 in a fixed order.  mod_kind as in attn_tree_fwd.
+ * A NaN LSE makes the totals of the slots that its query sees NaN; a NaN value
+ * of a key that of its own slot, and an infinite one may.
  * counts[b] is clamped to lens[b]; path entries outside [0, T) count for
  * nothing (both ATTN_ERR_INDEX).
  */

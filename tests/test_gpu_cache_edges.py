@@ -329,3 +329,34 @@ def test_tree_over_thousands_of_rows(ta, T):
     torch.cuda.synchronize()
     assert ta.attn_get_status() == 0
     check_tree(out, lse, tree_reference(c, None))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("path", [False, True])
+@pytest.mark.parametrize("T,Hq", [(6, 4), (150, 8)])
+def test_weights_of_values_that_are_not_finite(ta, D, path, T, Hq):
+    """A NaN key reaches its own slot's total alone, a NaN LSE the slots that its query sees."""
+    lens, counts = [400, T + 9], [T, T - 2]
+    c, p, lse, w = weights_case(T + D, lens, counts, T, Hq, 2, D, 64, path)
+
+    def call(lse):
+        out = torch.full((2, 2, c.cap), 7.0, device="cuda")
+        ta.attn_cache_weights(c.q_t, torch.from_numpy(lse).cuda(), c.cache, torch.from_numpy(w).cuda(), out, path=i32(p),
+                              counts=i32(counts), scale=c.scale)
+        torch.cuda.synchronize()
+        return out.cpu()
+
+    good = call(lse)
+    hit = torch.zeros(2, 2, c.cap, dtype=torch.bool)
+    for b, slot in ((0, 33), (0, 399), (1, T + 4)):  # an old one, the newest, one that only some queries see
+        c.k_t[int(c.table[b, slot // 64]), 1, slot % 64, 5] = NAN
+        hit[b, 1, slot] = True
+    got = call(lse)
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], good[~hit])
+    i = T // 2  # the accepted query whose LSE goes
+    lse = lse.copy()
+    lse[0, 0, i if p is None else int(p[0, i])] = NAN
+    hit[0, 0, : lens[0] - counts[0] + i + 1] = True
+    got = call(lse)
+    assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], good[~hit])
+    assert ta.attn_get_status() == 0

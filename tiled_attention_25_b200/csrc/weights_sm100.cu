@@ -21,7 +21,7 @@
 // of the units in (row, head, pair) order, Q staying in shared memory while
 // the head stays; with more, units in the order of their pair index over all
 // rows and heads, i.e. longest first under the causal limit, in a snake.
-// Prompts (no path) with fewer units than half the SMs are shared by clusters of
+// Prompts (no path) whose new tokens make fewer units than half the SMs are shared by clusters of
 // 2 to 8 CTAs, each of which takes every C-th Q tile of a unit; the sums meet in
 // the first CTA's shared memory and are added in the order of the CTAs.
 //
@@ -830,9 +830,11 @@ cudaError_t launch_cache_weights(const CUtensorMap& tq, const CUtensorMap& tk, c
   const int k_slots = tiles - (p.one_tile ? 1 : q_slots);
   p.k_slots[0] = (k_slots + 1) / 2;
   p.k_slots[1] = k_slots / 2;
-  // a prompt's units (its new tokens alone): shared while they fill less than half the SMs.
-  // Not with a path: accepted drafts are few queries over many more units than those, and
-  // each CTA of a cluster would read all their keys (28 of 15 rows 51 against 38 us)
+  // a prompt's units, counted from its new tokens alone (the filled lengths are on the device):
+  // shared while they fill less than half the SMs.  Not with a path: accepted drafts are few
+  // queries over many more units than those, and each CTA of a cluster would read all their
+  // keys (28 of 15 rows 51 against 38 us).  A chunk of a prompt, or a chain of drafts, over a
+  // filled cache has more units too, and is shared all the same
   p.split = 1;
   if (!p.one_tile && a.path == nullptr) {
     const long long units = static_cast<long long>(a.c.ix.B) * a.c.ix.Hkv * ((a.T + 2 * TILE - 1) / (2 * TILE));
